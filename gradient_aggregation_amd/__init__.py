@@ -20,7 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgradagg.so")
 
 GA_OK, GA_ERR_INVALID, GA_ERR_ALIGN, GA_ERR_DEVICE, GA_ERR_UNSUPPORTED = range(5)
-GA_FP32, GA_FP16 = 0, 1
+GA_FP32, GA_FP16, GA_BF16 = 0, 1, 2
 ORDERS = {"tree": 0, "server": 1, "ring": 2}
 MAX_WORKERS = 1024
 MAX_CHUNKS = 65536
@@ -55,6 +55,22 @@ class History(ctypes.Structure):
 
 _VP = ctypes.c_void_p
 _lib = None
+
+
+class AdamWParams(ctypes.Structure):
+    """ga_adamw_params."""
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("t", ctypes.c_int64)]
+
+
+class AdamWStatePtrs(ctypes.Structure):
+    """ga_adamw_state."""
+    _fields_ = [("m", _VP), ("v", _VP), ("m_scale", _VP), ("v_scale", _VP)]
+
+
+class Rows(ctypes.Structure):
+    """ga_rows: a row-major tensor and its row stride in elements."""
+    _fields_ = [("data", _VP), ("ld", ctypes.c_int64)]
 
 
 def lib() -> ctypes.CDLL:
@@ -127,6 +143,25 @@ def lib() -> ctypes.CDLL:
         L.ga_bucket_reduce_layers.restype = st
         L.ga_bucket_reduce_layers.argtypes = [_VP, ctypes.c_int32, _VP, _VP, _VP, ctypes.POINTER(SGD), _VP, _VP,
                                               ctypes.c_int32, _VP]
+        i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        rows = ctypes.POINTER(Rows)
+        L.ga_adamw_create.restype = st
+        L.ga_adamw_create.argtypes = [i32, i32, _VP, st, i32, _VP, ctypes.POINTER(_VP)]
+        L.ga_adamw_destroy.restype = None
+        L.ga_adamw_destroy.argtypes = [_VP]
+        L.ga_grad_norm.restype = st
+        L.ga_grad_norm.argtypes = [_VP, _VP, f32, _VP, _VP, _VP]
+        L.ga_adamw_step.restype = st
+        L.ga_adamw_step.argtypes = [_VP, _VP, ctypes.POINTER(AdamWParams), _VP, ctypes.POINTER(AdamWStatePtrs), _VP, _VP, st,
+                                    _VP]
+        L.ga_layernorm_create.restype = st
+        L.ga_layernorm_create.argtypes = [i64, st, st, i32, ctypes.POINTER(_VP)]
+        L.ga_layernorm_destroy.restype = None
+        L.ga_layernorm_destroy.argtypes = [_VP]
+        L.ga_layernorm_forward.restype = st
+        L.ga_layernorm_forward.argtypes = [_VP, i64, rows, rows, _VP, _VP, f32, rows, rows, _VP, _VP, _VP]
+        L.ga_layernorm_backward.restype = st
+        L.ga_layernorm_backward.argtypes = [_VP, i64, rows, rows, _VP, _VP, _VP, rows, rows, i32, _VP, _VP, st, _VP]
         _lib = L
     return _lib
 
@@ -562,3 +597,14 @@ def sgd_momentum_apply(grad, w, v, lr: float, mu: float) -> None:
     P = w.numel()
     _check(lib().ga_sgd_momentum_apply(P, _dev(grad, torch.float32, P, "grad"), _dev(w, torch.float32, P, "w"),
                                        _dev(v, torch.float32, P, "v"), ctypes.byref(SGD(lr, mu)), _stream_ptr()))
+
+
+_TRAINING = ("AdamW", "AdamWState", "Clip", "LayerNorm")
+
+
+def __getattr__(name: str):
+    # the training-step operators need torch, which the plan arithmetic above does not
+    if name in _TRAINING:
+        from . import training
+        return getattr(training, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

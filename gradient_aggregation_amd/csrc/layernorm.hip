@@ -1,0 +1,594 @@
+// Layer norm over rows, forward and backward (ga_layernorm_forward,
+// ga_layernorm_backward).
+//
+// Forward: a row is read once and stays in registers, spread over T threads as
+// V vectors of 16 bytes each; its mean and then the sum of squared deviations
+// from that mean are reduced across the threads, so a row far from zero loses
+// nothing.  Backward: one pass over the rows as well; each thread keeps the
+// weight and the two weight-gradient sums of its columns in registers over all
+// the rows its workgroup takes, and writes them as one partial row at the end.
+// A second kernel adds the partial rows of each group in a fixed order.
+//
+// Bound by memory: b * (2 to 4) bytes per element forward, b * (3 to 4)
+// backward, against some 15 to 25 instructions.
+#include <type_traits>
+
+#include "elements.h"
+#include "training.h"
+
+namespace ga {
+
+namespace {
+
+template <int X>
+constexpr int kVec = 16 / kSize<X>;     // elements of a 128-bit vector
+
+// Rows wider than this do not stay in registers: they are read again in each
+// pass (from the caches, at these lengths).
+constexpr int64_t kInRegisters = 16384;
+constexpr int kLongThreads = 1024;
+
+// Elements [c, c + N) of a row that ends at dim; those past it are 0.
+template <int X, int N>
+__device__ __forceinline__ void load_part(Raw<X, N>& r, uint64_t row, int64_t c, int64_t dim) {
+    const uint64_t at = row + (uint64_t)c * kSize<X>;
+    if (c + N <= dim) {
+        r.load(at);
+        return;
+    }
+    float f[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = 0.f;
+    if (c < dim) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (c + e < dim) f[e] = load_one<X>(at + e * kSize<X>);
+    }
+    r.narrow(f);
+}
+
+template <int X, int N>
+__device__ __forceinline__ void store_part(const float (&f)[N], uint64_t row, int64_t c, int64_t dim) {
+    const uint64_t at = row + (uint64_t)c * kSize<X>;
+    if (c + N <= dim) {
+        Raw<X, N> r;
+        r.narrow(f);
+        r.store(at);
+    } else if (c < dim) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (c + e < dim) store_one<X>(at + e * kSize<X>, f[e]);
+    }
+}
+
+// N elements of a weight vector from column c (fill where it is not given or
+// past dim).
+template <int P, int N>
+__device__ __forceinline__ void load_param(float (&f)[N], const void* p, int64_t c, int64_t dim, float fill) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = fill;
+    if (!p || c >= dim) return;
+    const uint64_t at = reinterpret_cast<uint64_t>(p) + (uint64_t)c * kSize<P>;
+    if (c + N <= dim) {
+        Raw<P, N> r;
+        r.load(at);
+        r.widen(f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (c + e < dim) f[e] = load_one<P>(at + e * kSize<P>);
+    }
+}
+
+// Sum over T threads (one wavefront, or the whole workgroup through LDS: buf
+// holds T / 64 values and must not be written again before the next barrier).
+template <int T>
+__device__ __forceinline__ float team_sum(float x, float* buf) {
+    x = wave_sum_f32(x);
+    if constexpr (T == 64) return x;
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float t = buf[0];
+#pragma unroll
+    for (int j = 1; j < T / 64; ++j) t += buf[j];
+    return t;
+}
+
+// T threads take a row; a workgroup of 256 takes 4 rows when T is a wavefront.
+template <int T>
+constexpr int kTeamRows = T == 64 ? 4 : 1;
+template <int T>
+constexpr int kTeamThreads = T == 64 ? 256 : T;
+
+template <int X, int P, int T, int V>
+__global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim) {
+    constexpr int N = kVec<X>, R = kTeamRows<T>;
+    __shared__ float red[2][T / 64];
+    const int t = threadIdx.x % T;
+    float gamma[V][N], beta[V][N];
+    int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / T;
+    Raw<X, N> x[V], r[V];
+    auto load_row = [&](int64_t row) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + t) * N;
+            load_part(x[v], reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx), c, dim);
+            if (a.res) load_part(r[v], reinterpret_cast<uint64_t>(a.res) + (uint64_t)(row * a.ldr), c, dim);
+        }
+    };
+    if (row < a.rows) load_row(row);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        load_param<P>(gamma[v], a.gamma, (v * T + t) * N, dim, 1.f);
+        load_param<P>(beta[v], a.beta, (v * T + t) * N, dim, 0.f);
+    }
+    const float inv_dim = (float)(1.0 / (double)dim);
+    for (; row < a.rows; row += (int64_t)gridDim.x * R) {
+        float f[V][N];
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v].widen(f[v]);
+            if (a.res) {
+                float h[N];
+                r[v].widen(h);
+                // the sum is rounded to x's type, as it is stored, before it is normalised
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[v][e] = f[v][e] + h[e];
+                Raw<X, N> s;
+                s.narrow(f[v]);
+                s.widen(f[v]);
+                if (a.sum)
+                    store_part<X>(f[v], reinterpret_cast<uint64_t>(a.sum) + (uint64_t)(row * a.lds), (v * T + t) * N,
+                                  dim);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum += f[v][e];
+        }
+        const int64_t next = row + (int64_t)gridDim.x * R;
+        if (next < a.rows) load_row(next);
+        const float mean = team_sum<T>(sum, red[0]) * inv_dim;
+        float sq = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int left = dim - (v * T + t) * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[v][e] -= mean;
+            if (left >= N) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) sq = fmaf(f[v][e], f[v][e], sq);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (e < left) sq = fmaf(f[v][e], f[v][e], sq);
+            }
+        }
+        const float var = team_sum<T>(sq, red[1]) * inv_dim;
+        const float rstd = 1.f / sqrtf(var + a.eps);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[v][e] = fmaf(f[v][e] * rstd, gamma[v][e], beta[v][e]);
+            store_part<X>(f[v], reinterpret_cast<uint64_t>(a.y) + (uint64_t)(row * a.ldy), (v * T + t) * N, dim);
+        }
+        if (t == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// Rows that do not stay in registers: a workgroup per row, three passes.
+template <int X, int P>
+__global__ __launch_bounds__(kLongThreads) void k_ln_fwd_long(LnFwd a, int64_t dim) {
+    constexpr int N = kVec<X>, T = kLongThreads;
+    __shared__ float red[2][T / 64];
+    const float inv_dim = (float)(1.0 / (double)dim);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const uint64_t xr = reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx);
+        const uint64_t rr = reinterpret_cast<uint64_t>(a.res) + (uint64_t)(row * a.ldr);
+        const uint64_t sr = reinterpret_cast<uint64_t>(a.sum) + (uint64_t)(row * a.lds);
+        const uint64_t yr = reinterpret_cast<uint64_t>(a.y) + (uint64_t)(row * a.ldy);
+        auto value = [&](int64_t c, float (&f)[N]) {
+            Raw<X, N> x;
+            load_part(x, xr, c, dim);
+            x.widen(f);
+            if (a.res) {
+                float h[N];
+                load_part(x, rr, c, dim);
+                x.widen(h);
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[e] = rounded<X>(f[e] + h[e]);
+            }
+        };
+        // y or sum may be x or the residual: the later passes read the sum
+        // where it was stored, else form it again (y is written last)
+        auto again = [&](int64_t c, float (&f)[N]) {
+            if (a.res && a.sum) {
+                Raw<X, N> x;
+                load_part(x, sr, c, dim);
+                x.widen(f);
+            } else {
+                value(c, f);
+            }
+        };
+        float sum = 0.f;
+        for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
+            float f[N];
+            value(c, f);
+            if (a.res && a.sum) store_part<X>(f, sr, c, dim);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum += f[e];
+        }
+        const float mean = team_sum<T>(sum, red[0]) * inv_dim;
+        float sq = 0.f;
+        for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
+            float f[N];
+            again(c, f);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (c + e < dim) sq = fmaf(f[e] - mean, f[e] - mean, sq);
+        }
+        const float var = team_sum<T>(sq, red[1]) * inv_dim;
+        const float rstd = 1.f / sqrtf(var + a.eps);
+        for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
+            float f[N], gamma[N], beta[N];
+            again(c, f);
+            load_param<P>(gamma, a.gamma, c, dim, 1.f);
+            load_param<P>(beta, a.beta, c, dim, 0.f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[e] = fmaf((f[e] - mean) * rstd, gamma[e], beta[e]);
+            store_part<X>(f, yr, c, dim);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// Where a workgroup's weight-gradient sums go: straight to the result when its
+// group has one part, else to its partial row.
+__device__ __forceinline__ void store_param(void* out, int32_t dtype, int64_t i, float x) {
+    if (dtype == kF32) static_cast<float*>(out)[i] = x;
+    else if (dtype == kF16) store_one<kF16>(reinterpret_cast<uint64_t>(out) + (uint64_t)i * 2, x);
+    else store_one<kB16>(reinterpret_cast<uint64_t>(out) + (uint64_t)i * 2, x);
+}
+
+// Workgroup blockIdx.x = group * parts + part takes rows part * R, (part +
+// parts) * R, ... of its group, R at a time.
+template <int X, int P, int T, int V>
+__global__ __launch_bounds__(kTeamThreads<T>) void k_ln_bwd(LnBwd a, int32_t dim, int64_t ldp, int32_t parts,
+                                                            float* __restrict__ out) {
+    constexpr int N = kVec<X>, R = kTeamRows<T>;
+    __shared__ float red[2][2][T / 64];
+    const int t = threadIdx.x % T;
+    const int32_t group = (int32_t)(blockIdx.x / (uint32_t)parts), part = (int32_t)(blockIdx.x % (uint32_t)parts);
+    const int64_t row0 = (int64_t)group * a.group_rows, row1 = row0 + a.group_rows;
+    const int64_t step = (int64_t)parts * R;
+    int64_t row = row0 + (int64_t)part * R + threadIdx.x / T;
+
+    Raw<X, N> xr[V], yr[V], sr[V];
+    float mean = 0.f, rstd = 0.f;
+    auto load_row = [&](int64_t row) {
+        mean = a.mean[row];
+        rstd = a.rstd[row];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + t) * N;
+            load_part(xr[v], reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx), c, dim);
+            load_part(yr[v], reinterpret_cast<uint64_t>(a.dy) + (uint64_t)(row * a.ldy), c, dim);
+            if (a.dsum) load_part(sr[v], reinterpret_cast<uint64_t>(a.dsum) + (uint64_t)(row * a.lds), c, dim);
+        }
+    };
+    if (row < row1) load_row(row);
+    float gamma[V][N], dg[V][N], db[V][N];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        load_param<P>(gamma[v], a.gamma, (v * T + t) * N, dim, 1.f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) dg[v][e] = db[v][e] = 0.f;
+    }
+    const float inv_dim = (float)(1.0 / (double)dim);
+    int parity = 0;
+    for (; row < row1; row += step) {
+        float xh[V][N], h[V][N], ds[V][N];
+        float s1 = 0.f, s2 = 0.f;
+        const float rs = rstd;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float dy[N];
+            xr[v].widen(xh[v]);
+            yr[v].widen(dy);
+            if (a.dsum) {
+                sr[v].widen(ds[v]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) ds[v][e] = 0.f;
+            }
+            // columns past dim hold dy = 0 and add nothing anywhere
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                xh[v][e] = (xh[v][e] - mean) * rs;
+                dg[v][e] = fmaf(dy[e], xh[v][e], dg[v][e]);
+                db[v][e] += dy[e];
+                h[v][e] = dy[e] * gamma[v][e];
+                s1 += h[v][e];
+                s2 = fmaf(h[v][e], xh[v][e], s2);
+            }
+        }
+        if (row + step < row1) load_row(row + step);
+        s1 = wave_sum_f32(s1);
+        s2 = wave_sum_f32(s2);
+        if constexpr (T > 64) {
+            if ((threadIdx.x & 63) == 0) {
+                red[parity][0][threadIdx.x >> 6] = s1;
+                red[parity][1][threadIdx.x >> 6] = s2;
+            }
+            __syncthreads();
+            s1 = red[parity][0][0];
+            s2 = red[parity][1][0];
+#pragma unroll
+            for (int j = 1; j < T / 64; ++j) {
+                s1 += red[parity][0][j];
+                s2 += red[parity][1][j];
+            }
+            parity ^= 1;
+        }
+        s1 *= inv_dim;
+        s2 *= inv_dim;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) h[v][e] = fmaf(rs, h[v][e] - fmaf(xh[v][e], s2, s1), ds[v][e]);
+            store_part<X>(h[v], reinterpret_cast<uint64_t>(a.dx) + (uint64_t)(row * a.ldd), (v * T + t) * N, dim);
+        }
+    }
+    if (!a.dgamma) return;
+    float* pg = out + (int64_t)blockIdx.x * 2 * ldp;
+    if constexpr (T == 64) {
+        // the four wavefronts' sums, added in order
+        __shared__ float cols[4][V * 64 * N];
+        const int wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) cols[wave][(v * 64 + t) * N + e] = which ? db[v][e] : dg[v][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < dim; c += 256) {
+                const float s = ((cols[0][c] + cols[1][c]) + cols[2][c]) + cols[3][c];
+                if (parts == 1) store_param(which ? a.dbeta : a.dgamma, a.dp_dtype, (int64_t)group * dim + c, s);
+                else pg[which * ldp + c] = s;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int c = (v * T + t) * N + e;
+                if (c >= dim) continue;
+                if (parts == 1) {
+                    store_param(a.dgamma, a.dp_dtype, (int64_t)group * dim + c, dg[v][e]);
+                    store_param(a.dbeta, a.dp_dtype, (int64_t)group * dim + c, db[v][e]);
+                } else {
+                    pg[c] = dg[v][e];
+                    pg[ldp + c] = db[v][e];
+                }
+            }
+        }
+    }
+}
+
+// Rows that do not stay in registers: dx with two passes over the row ...
+template <int X, int P>
+__global__ __launch_bounds__(kLongThreads) void k_ln_dx_long(LnBwd a, int64_t dim) {
+    constexpr int N = kVec<X>, T = kLongThreads;
+    __shared__ float red[2][T / 64];
+    const float inv_dim = (float)(1.0 / (double)dim);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float mean = a.mean[row], rs = a.rstd[row];
+        float s1 = 0.f, s2 = 0.f;
+        auto parts = [&](int64_t c, float (&xh)[N], float (&h)[N]) {
+            Raw<X, N> r;
+            float gamma[N];
+            load_part(r, reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx), c, dim);
+            r.widen(xh);
+            load_part(r, reinterpret_cast<uint64_t>(a.dy) + (uint64_t)(row * a.ldy), c, dim);
+            r.widen(h);
+            load_param<P>(gamma, a.gamma, c, dim, 1.f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                xh[e] = (xh[e] - mean) * rs;
+                h[e] *= gamma[e];
+            }
+        };
+        for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
+            float xh[N], h[N];
+            parts(c, xh, h);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                s1 += h[e];
+                s2 = fmaf(h[e], xh[e], s2);
+            }
+        }
+        __syncthreads();   // the previous row's sums are read
+        s1 = team_sum<T>(s1, red[0]) * inv_dim;
+        s2 = team_sum<T>(s2, red[1]) * inv_dim;
+        for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
+            float xh[N], h[N], ds[N];
+            parts(c, xh, h);
+#pragma unroll
+            for (int e = 0; e < N; ++e) ds[e] = 0.f;
+            if (a.dsum) {
+                Raw<X, N> r;
+                load_part(r, reinterpret_cast<uint64_t>(a.dsum) + (uint64_t)(row * a.lds), c, dim);
+                r.widen(ds);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) h[e] = fmaf(rs, h[e] - fmaf(xh[e], s2, s1), ds[e]);
+            store_part<X>(h, reinterpret_cast<uint64_t>(a.dx) + (uint64_t)(row * a.ldd), c, dim);
+        }
+    }
+}
+
+// ... and the weight gradients with a thread per column, over the rows of part
+// blockIdx.y of its group.
+template <int X>
+__global__ __launch_bounds__(256) void k_ln_params_long(LnBwd a, int64_t dim, int64_t ldp, int32_t parts,
+                                                        float* __restrict__ out) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= dim) return;
+    const int32_t group = (int32_t)(blockIdx.y / (uint32_t)parts), part = (int32_t)(blockIdx.y % (uint32_t)parts);
+    const int64_t row1 = (int64_t)(group + 1) * a.group_rows;
+    float dg = 0.f, db = 0.f;
+    for (int64_t row = (int64_t)group * a.group_rows + part; row < row1; row += parts) {
+        const float x = load_one<X>(reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx + c * kSize<X>));
+        const float dy = load_one<X>(reinterpret_cast<uint64_t>(a.dy) + (uint64_t)(row * a.ldy + c * kSize<X>));
+        dg = fmaf(dy, (x - a.mean[row]) * a.rstd[row], dg);
+        db += dy;
+    }
+    if (parts == 1) {
+        store_param(a.dgamma, a.dp_dtype, (int64_t)group * dim + c, dg);
+        store_param(a.dbeta, a.dp_dtype, (int64_t)group * dim + c, db);
+    } else {
+        out[(int64_t)blockIdx.y * 2 * ldp + c] = dg;
+        out[((int64_t)blockIdx.y * 2 + 1) * ldp + c] = db;
+    }
+}
+
+// Adds the `parts` partial rows of group blockIdx.y in a fixed order: 16
+// threads take every 16th part of 64 columns, then the 16 sums are added.
+// parts = 0 writes zeros.
+__global__ __launch_bounds__(256) void k_ln_params_end(const float* __restrict__ in, int64_t dim, int64_t ldp,
+                                                       int32_t parts, void* dgamma, void* dbeta, int32_t dp_dtype) {
+    __shared__ f32x4 sums[16][16];
+    const int quad = threadIdx.x & 15, slice = threadIdx.x >> 4;
+    const int64_t c4 = ((int64_t)blockIdx.x * 16 + quad) * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (c4 < 2 * ldp) {
+        const float* p = in + (int64_t)blockIdx.y * parts * 2 * ldp + c4;
+#pragma unroll 4
+        for (int32_t k = slice; k < parts; k += 16) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(p + (int64_t)k * 2 * ldp);
+            s.x += x.x;
+            s.y += x.y;
+            s.z += x.z;
+            s.w += x.w;
+        }
+    }
+    sums[slice][quad] = s;
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    if (c >= 2 * ldp) return;
+    const float* f = reinterpret_cast<const float*>(sums);
+    float t = f[threadIdx.x];
+    for (int k = 1; k < 16; ++k) t += f[k * 64 + threadIdx.x];
+    const int64_t col = c < ldp ? c : c - ldp;
+    if (col >= dim) return;
+    store_param(c < ldp ? dgamma : dbeta, dp_dtype, (int64_t)blockIdx.y * dim + col, t);
+}
+
+// Calls f<T, V> with the team that holds a row of dim elements.
+template <int X, typename F>
+hipError_t with_team(int64_t dim, F f) {
+#define GA_TEAM(T, V) \
+    if (dim <= T * V * kVec<X>) return f(std::integral_constant<int, T>{}, std::integral_constant<int, V>{})
+    if constexpr (X == kF32) {
+        GA_TEAM(64, 1);
+        GA_TEAM(64, 2);
+        GA_TEAM(64, 4);
+        GA_TEAM(256, 2);
+        GA_TEAM(256, 4);
+        GA_TEAM(512, 4);
+        GA_TEAM(1024, 4);
+    } else {
+        GA_TEAM(64, 1);
+        GA_TEAM(64, 2);
+        GA_TEAM(256, 1);
+        GA_TEAM(256, 2);
+        GA_TEAM(512, 2);
+        GA_TEAM(1024, 2);
+    }
+#undef GA_TEAM
+    return hipErrorInvalidValue;
+}
+
+constexpr int64_t kFwdBlocks = 2048;   // workgroups of 256 threads that fill the chip
+
+template <int X, int P>
+hipError_t ln_fwd(const LayerNorm& n, const LnFwd& a, hipStream_t s) {
+    if (n.dim > kInRegisters) {
+        const unsigned blocks = (unsigned)(a.rows < 1024 ? a.rows : 1024);
+        hipLaunchKernelGGL((k_ln_fwd_long<X, P>), dim3(blocks), dim3(kLongThreads), 0, s, a, n.dim);
+        return hipGetLastError();
+    }
+    return with_team<X>(n.dim, [&](auto t, auto v) {
+        constexpr int T = decltype(t)::value, V = decltype(v)::value;
+        const int64_t want = (a.rows + kTeamRows<T> - 1) / kTeamRows<T>;
+        const int64_t most = kFwdBlocks * 256 / kTeamThreads<T>;
+        hipLaunchKernelGGL((k_ln_fwd<X, P, T, V>), dim3((unsigned)(want < most ? want : most)),
+                           dim3(kTeamThreads<T>), 0, s, a, (int32_t)n.dim);
+        return hipGetLastError();
+    });
+}
+
+// Parts of each group: enough workgroups to fill the chip, at most one per
+// row-set and kLnParts in all.
+inline int32_t parts_of(const LnBwd& a, int rows_at_once, int64_t most) {
+    int64_t p = (a.group_rows + rows_at_once - 1) / rows_at_once;
+    if (p > most / a.groups) p = most / a.groups;
+    return p < 1 ? 1 : (int32_t)p;
+}
+
+template <int X, int P>
+hipError_t ln_bwd(const LayerNorm& n, const LnBwd& a, hipStream_t s) {
+    int32_t parts = 0;
+    hipError_t e = hipSuccess;
+    if (a.rows > 0 && n.dim > kInRegisters) {
+        if (a.dgamma) {
+            parts = parts_of(a, 64, kLnParts);
+            hipLaunchKernelGGL((k_ln_params_long<X>), dim3((unsigned)((n.dim + 255) / 256), (unsigned)(a.groups * parts)),
+                               dim3(256), 0, s, a, n.dim, n.ldp, parts, n.d_parts);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        const unsigned blocks = (unsigned)(a.rows < 1024 ? a.rows : 1024);
+        hipLaunchKernelGGL((k_ln_dx_long<X, P>), dim3(blocks), dim3(kLongThreads), 0, s, a, n.dim);
+        e = hipGetLastError();
+    } else if (a.rows > 0) {
+        e = with_team<X>(n.dim, [&](auto t, auto v) {
+            constexpr int T = decltype(t)::value, V = decltype(v)::value;
+            parts = parts_of(a, kTeamRows<T>, kLnParts);
+            hipLaunchKernelGGL((k_ln_bwd<X, P, T, V>), dim3((unsigned)(a.groups * parts)), dim3(kTeamThreads<T>), 0, s,
+                               a, (int32_t)n.dim, n.ldp, parts, n.d_parts);
+            return hipGetLastError();
+        });
+    }
+    if (e != hipSuccess || !a.dgamma || parts == 1) return e;
+    hipLaunchKernelGGL(k_ln_params_end, dim3((unsigned)((2 * n.ldp + 63) / 64), (unsigned)a.groups), dim3(256), 0, s,
+                       n.d_parts, n.dim, n.ldp, parts, a.dgamma, a.dbeta, a.dp_dtype);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_ln_fwd(const LayerNorm& n, const LnFwd& a, hipStream_t s) {
+    if (n.x_dtype == GA_FP32) return ln_fwd<kF32, kF32>(n, a, s);
+    if (n.x_dtype == GA_FP16)
+        return n.p_dtype == GA_FP32 ? ln_fwd<kF16, kF32>(n, a, s) : ln_fwd<kF16, kF16>(n, a, s);
+    return n.p_dtype == GA_FP32 ? ln_fwd<kB16, kF32>(n, a, s) : ln_fwd<kB16, kB16>(n, a, s);
+}
+
+hipError_t launch_ln_bwd(const LayerNorm& n, const LnBwd& a, hipStream_t s) {
+    if (n.x_dtype == GA_FP32) return ln_bwd<kF32, kF32>(n, a, s);
+    if (n.x_dtype == GA_FP16)
+        return n.p_dtype == GA_FP32 ? ln_bwd<kF16, kF32>(n, a, s) : ln_bwd<kF16, kF16>(n, a, s);
+    return n.p_dtype == GA_FP32 ? ln_bwd<kB16, kF32>(n, a, s) : ln_bwd<kB16, kB16>(n, a, s);
+}
+
+}  // namespace ga

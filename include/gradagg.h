@@ -84,7 +84,9 @@ typedef enum {
     GA_ERR_UNSUPPORTED = 4
 } ga_status;
 
-typedef enum { GA_FP32 = 0, GA_FP16 = 1 } ga_dtype;
+/* GA_BF16 (bfloat16) is an element type of the training-step operators
+   (ga_adamw, ga_layernorm); a ga_plan's gradients are GA_FP32 or GA_FP16. */
+typedef enum { GA_FP32 = 0, GA_FP16 = 1, GA_BF16 = 2 } ga_dtype;
 
 /* Summation orders of ga_reduce_variant. */
 typedef enum { GA_ORDER_TREE = 0, GA_ORDER_SERVER = 1, GA_ORDER_RING = 2 } ga_order;
@@ -482,6 +484,175 @@ ga_status ga_bucket_range(const ga_buckets* buckets, int32_t b, int32_t* first_l
 ga_status ga_bucket_reduce_layers(const ga_buckets* buckets, int32_t b, const uint64_t* d_layer_ptrs,
                                   hipEvent_t ready, float* d_grad, const ga_sgd* sgd, float* d_w, float* d_v,
                                   int32_t max_workgroups, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Training-step operators: what a step does around the aggregation.  A
+ * gradient norm over every layer (for clipping), the AdamW update of all
+ * layers in one launch, and layer norm forward and backward.
+ * ---------------------------------------------------------------------- */
+
+/* Consecutive elements of the fused vector that share a scale in 8-bit states. */
+#define GA_STATE_BLOCK 256
+
+/* AdamW hyper-parameters.  t: the step, counted from 1. */
+typedef struct {
+    float lr;
+    float beta1;
+    float beta2;
+    float eps;
+    float weight_decay;
+    int64_t t;
+} ga_adamw_params;
+
+/*
+ * Optimizer state of the P parameters.
+ *   32 bits: m, v [P] binary32, the moments themselves; scales unused (NULL).
+ *   8 bits:  m, v [n_b][GA_STATE_BLOCK] e4m3 codes (bias 7, largest 448, no
+ *            infinity), n_b = ceil(P / GA_STATE_BLOCK), each block with a
+ *            binary32 scale in m_scale, v_scale [n_b].  A code stands for
+ *            code * scale; m holds the first moment, v the SQUARE ROOT of the
+ *            second (its range in powers of two is half as wide).  Codes past P
+ *            are zero.
+ * All zero is the state before the first step, in both forms.
+ */
+typedef struct {
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+} ga_adamw_state;
+
+/* What ga_grad_norm leaves on the device for ga_adamw_step (16 bytes). */
+typedef struct {
+    float norm;     /* L2 norm of the mean gradient */
+    float scale;    /* min(1, max_norm / norm) */
+    int32_t skip;   /* 1 when the norm is not finite: the step changes nothing */
+    int32_t unused;
+} ga_clip;
+
+typedef struct ga_adamw ga_adamw;
+
+/*
+ * Handle for W workers and a layer list, on the current device: W,
+ * n_layers and layer_numel as in ga_plan_create.
+ *   grad_dtype: GA_FP32, GA_FP16 or GA_BF16 (GA_ERR_INVALID otherwise).
+ *   state_bits: 32 or 8 (GA_ERR_INVALID otherwise).
+ *   decay:      n_layers bytes on the host, nonzero where weight decay applies
+ *               to the layer; NULL for every layer.
+ * The handle owns small device tables and the workspace of ga_grad_norm.  The
+ * calls below allocate nothing, do not synchronize and may be captured into a
+ * graph (the parameters are then those of the capture).  Steps on one handle
+ * may run at the same time; two ga_grad_norm calls may not (issue them on one
+ * stream or order them with events).
+ */
+ga_status ga_adamw_create(int32_t W, int32_t n_layers, const int64_t* layer_numel, ga_dtype grad_dtype,
+                          int32_t state_bits, const uint8_t* decay, ga_adamw** out);
+
+/* Destroy a handle (NULL is ignored).  No call using it may still be queued. */
+void ga_adamw_destroy(ga_adamw* opt);
+
+/*
+ * L2 norm of the mean gradient over all layers:
+ *   g[i] = T(0, W) * fl32(1/W) over the workers (the tree of ga_tree_reduce,
+ *          binary32),  norm = sqrt(sum g[i]^2), summed in binary64 in a fixed
+ *          order and rounded once,
+ *   d_clip <- {norm, min(1, max_norm / norm), norm is not finite}.
+ * d_layer_ptrs: as in ga_bucket_pack, elements of grad_dtype, each tensor
+ *   aligned to its element.  d_grad: [P] binary32 output for g, or NULL.
+ * max_norm > 0 (infinity: only measure).  GA_ERR_ALIGN: d_clip and d_grad
+ * must be 16-byte aligned.
+ */
+ga_status ga_grad_norm(const ga_adamw* opt, const uint64_t* d_layer_ptrs, float max_norm, float* d_grad,
+                       ga_clip* d_clip, hipStream_t stream);
+
+/*
+ * AdamW step of all layers in one launch.  With g the mean gradient of
+ * ga_grad_norm, times d_clip->scale where d_clip is given:
+ *   m <- beta1 m + (1 - beta1) g          v <- beta2 v + (1 - beta2) g^2
+ *   w <- w (1 - lr * weight_decay) - lr/(1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * (weight_decay taken as 0 on the layers without decay), in binary32; the new
+ * w is also rounded into d_copy.  Where d_clip->skip is set, nothing is
+ * written.  8-bit states: a block's new moments are scaled by 448 over their
+ * largest magnitude (at least 2^-100); m is rounded to nearest even; v's root
+ * is raised to 2^-6 of the scaled range where it is not zero (so that it never
+ * rounds to zero under a gradient) and rounded up or down at random, with bits
+ * that are a fixed function of the element's index and t, so that a second
+ * moment that moves by less than a code's step per step still moves on average.
+ *   d_w: [P] binary32 in/out.  d_copy: [P] of copy_dtype (GA_FP16 or
+ *   GA_BF16), or NULL.  d_clip: NULL or a record of ga_grad_norm.
+ * Errors: GA_ERR_INVALID (NULL argument, a missing scale, t < 1, beta1 or
+ * beta2 outside [0, 1), lr, eps or weight_decay negative or not finite, a
+ * copy of another type), GA_ERR_ALIGN (d_w, m, v, d_copy and d_clip 16 bytes,
+ * scales 4 bytes), GA_ERR_DEVICE.
+ */
+ga_status ga_adamw_step(const ga_adamw* opt, const uint64_t* d_layer_ptrs, const ga_adamw_params* params,
+                        float* d_w, const ga_adamw_state* state, const ga_clip* d_clip, void* d_copy,
+                        ga_dtype copy_dtype, hipStream_t stream);
+
+typedef struct ga_layernorm ga_layernorm;
+
+/* Most groups of a layer-norm backward pass. */
+#define GA_MAX_GROUPS GA_MAX_WORKERS
+/* Widest row of a layer norm. */
+#define GA_MAX_DIM ((int64_t)1 << 20)
+
+/*
+ * Layer norm over rows of dim elements of x_dtype, with weight and bias
+ * vectors of p_dtype (GA_FP32 or x_dtype), on the current device.  The handle
+ * owns the workspace of the backward pass's weight gradients: 512 partial rows
+ * of each, 4096 * (dim rounded up to 4) bytes, unless backward == 0 (then
+ * ga_layernorm_backward refuses the handle).
+ * GA_ERR_INVALID: dim < 1 or a type that is not listed; GA_ERR_UNSUPPORTED:
+ * dim > GA_MAX_DIM.
+ */
+ga_status ga_layernorm_create(int64_t dim, ga_dtype x_dtype, ga_dtype p_dtype, int32_t backward,
+                              ga_layernorm** out);
+
+/* Destroy a handle (NULL is ignored).  No call using it may still be queued. */
+void ga_layernorm_destroy(ga_layernorm* ln);
+
+/* A row-major tensor: row r starts at data + r * ld elements (ld >= dim when
+   there is more than one row).  Aligned to its element. */
+typedef struct {
+    const void* data;
+    int64_t ld;
+} ga_rows;
+
+/*
+ * Forward over `rows` rows (0: nothing is launched):
+ *   s = x, or fl(x + residual) rounded to x_dtype when residual->data is given
+ *   mean = sum(s)/dim, rstd = 1/sqrt(sum((s - mean)^2)/dim + eps)   (binary32)
+ *   y = (s - mean) * rstd * gamma + beta, rounded once to x_dtype
+ * residual and sum: NULL, or rows of x_dtype; sum receives s.  gamma, beta:
+ * [dim] of p_dtype, or NULL for 1 and 0.  d_mean, d_rstd: [rows] binary32, or
+ * NULL.  y may be x or residual itself, and so may sum; y and sum must differ.
+ * GA_ERR_INVALID: NULL x or y, rows < 0, an ld shorter than a row, eps not
+ * positive and finite; GA_ERR_ALIGN: a tensor not aligned to its element.
+ */
+ga_status ga_layernorm_forward(const ga_layernorm* ln, int64_t rows, const ga_rows* x, const ga_rows* residual,
+                               const void* d_gamma, const void* d_beta, float eps, const ga_rows* y,
+                               const ga_rows* sum, float* d_mean, float* d_rstd, hipStream_t stream);
+
+/*
+ * Backward over the same rows.  With xh = (x - mean) * rstd and h = dy * gamma:
+ *   dx = rstd * (h - mean_row(h) - xh * mean_row(h * xh)) + dsum
+ *   dgamma[j] = sum of dy * xh,  dbeta[j] = sum of dy   over the rows of group j
+ * x is the s of the forward pass, dsum (NULL, or rows of x_dtype) the gradient
+ * that reaches s by other paths.  The rows form `groups` runs of rows/groups
+ * consecutive rows (one per worker, say), each with its own weight gradients:
+ * d_dgamma, d_dbeta: [groups][dim] of dp_dtype (any ga_dtype), or both NULL.
+ * Row sums and the weight gradients' sums are binary32, each in a fixed order.
+ * With rows = 0, zeros are written to them.  dx may be dy, dsum or x itself.
+ * Uses the handle's workspace: not concurrently with another backward pass on
+ * the same handle (issue them on one stream or order them with events).
+ * Errors as ga_layernorm_forward, and GA_ERR_INVALID when groups < 1 or does
+ * not divide rows, or only one of d_dgamma and d_dbeta is given;
+ * GA_ERR_UNSUPPORTED for groups > GA_MAX_GROUPS.
+ */
+ga_status ga_layernorm_backward(const ga_layernorm* ln, int64_t rows, const ga_rows* dy, const ga_rows* x,
+                                const void* d_gamma, const float* d_mean, const float* d_rstd, const ga_rows* dsum,
+                                const ga_rows* dx, int32_t groups, void* d_dgamma, void* d_dbeta, ga_dtype dp_dtype,
+                                hipStream_t stream);
 
 #ifdef __cplusplus
 }
