@@ -33,8 +33,9 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 
 // 4 consecutive binary32 values at element i of p, 0 past P.
-__device__ __forceinline__ f32x4 load4(const float* p, int64_t i, int64_t P) {
-    if (i + 4 <= P) return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i));
+template <bool WHOLE>
+__device__ __forceinline__ f32x4 load4(const float* p, int i, int64_t P) {
+    if (WHOLE || i + 4 <= P) return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i));
     f32x4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -42,8 +43,9 @@ __device__ __forceinline__ f32x4 load4(const float* p, int64_t i, int64_t P) {
     return r;
 }
 
-__device__ __forceinline__ void store4(float* p, int64_t i, int64_t P, const f32x4& x) {
-    if (i + 4 <= P) {
+template <bool WHOLE>
+__device__ __forceinline__ void store4(float* p, int i, int64_t P, const f32x4& x) {
+    if (WHOLE || i + 4 <= P) {
         __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(p + i));
     } else {
 #pragma unroll
@@ -52,10 +54,10 @@ __device__ __forceinline__ void store4(float* p, int64_t i, int64_t P, const f32
     }
 }
 
-template <int T>
-__device__ __forceinline__ void store4_narrow(void* p, int64_t i, int64_t P, const f32x4& x) {
-    const uint64_t at = reinterpret_cast<uint64_t>(p) + (uint64_t)i * 2;
-    if (i + 4 <= P) {
+template <int T, bool WHOLE>
+__device__ __forceinline__ void store4_narrow(void* p, int64_t e0, int i, int64_t P, const f32x4& x) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p) + (uint64_t)e0 * 2 + (uint32_t)i * 2;
+    if (WHOLE || i + 4 <= P) {
         Raw<T, 4> r;
         r.narrow({x.x, x.y, x.z, x.w});
         r.template store<true>(at);
@@ -66,14 +68,33 @@ __device__ __forceinline__ void store4_narrow(void* p, int64_t i, int64_t P, con
     }
 }
 
-template <int T, int BITS, int LEV, bool SPLIT>
-__global__ __launch_bounds__(kThreads) void k_adamw(GradArgs ga, StepArgs a, int64_t n_tiles) {
-    const int lane = threadIdx.x & 63;
-    const int64_t tile = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (tile >= n_tiles) return;
-    const TileRec rec = ga.tiles[tile];
-    const int64_t i0 = group_at<SPLIT>(tile, lane, 0), i1 = group_at<SPLIT>(tile, lane, 1);
-    const int64_t at[2] = {i0, i1};
+// Square roots of 8 values >= 0.  The hardware instruction is within 1 ulp
+// (1.54 half steps over 2^20 values of every exponent) but takes denormal
+// values for zero, which only matters when one is there: then the small values
+// are scaled up by 2^64 and the roots back by 2^-32, both exact.
+__device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
+    uint32_t low = __float_as_uint(v[0]);
+#pragma unroll
+    for (int e = 1; e < 8; ++e) low = __float_as_uint(v[e]) < low ? __float_as_uint(v[e]) : low;
+    if (low >= 0x00800000u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = __builtin_amdgcn_sqrtf(v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool small = v[e] < 0x1p-64f;
+            r[e] = __builtin_amdgcn_sqrtf(v[e] * (small ? 0x1p64f : 1.f)) * (small ? 0x1p-32f : 1.f);
+        }
+    }
+}
+
+// One tile.  WHOLE: it lies in one layer and inside P.
+template <int T, int BITS, int LEV, bool WHOLE>
+__device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a, int64_t tile, const TileRec& rec,
+                                           int lane) {
+    const int64_t e0 = tile * kTile;
+    const int at[2] = {lane * 4, 256 + lane * 4};   // from e0
+    const int64_t P = WHOLE ? (int64_t)kTile : ga.P - e0;
     float clip = 1.f;
     if (a.clip) {
         if (a.clip->skip) return;
@@ -83,32 +104,34 @@ __global__ __launch_bounds__(kThreads) void k_adamw(GradArgs ga, StepArgs a, int
     f32x4 w[2], m[2], s[2];   // s: v for binary32 moments, its root for codes
     float ms[2], vs[2];
     uint32_t mc[2], vc[2];
-    const int64_t n_coded = (ga.P + GA_STATE_BLOCK - 1) / GA_STATE_BLOCK * GA_STATE_BLOCK;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        w[q] = load4(a.w, at[q], ga.P);
+        w[q] = load4<WHOLE>(a.w + e0, at[q], P);
         if constexpr (BITS == 32) {
-            m[q] = load4(static_cast<const float*>(a.m), at[q], ga.P);
-            s[q] = load4(static_cast<const float*>(a.v), at[q], ga.P);
+            m[q] = load4<WHOLE>(static_cast<const float*>(a.m) + e0, at[q], P);
+            s[q] = load4<WHOLE>(static_cast<const float*>(a.v) + e0, at[q], P);
         } else {
             mc[q] = vc[q] = 0u;
             ms[q] = vs[q] = 0.f;
-            if (at[q] < n_coded) {
-                mc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + at[q]);
-                vc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + at[q]);
-                ms[q] = a.m_scale[at[q] / GA_STATE_BLOCK];
-                vs[q] = a.v_scale[at[q] / GA_STATE_BLOCK];
+            if (WHOLE || q * GA_STATE_BLOCK < P) {
+                mc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + e0 + at[q]);
+                vc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + e0 + at[q]);
+                ms[q] = a.m_scale[tile * 2 + q];
+                vs[q] = a.v_scale[tile * 2 + q];
             }
         }
     }
 
     float g[8];
-    uint32_t dmask;
-    mean_grad<T, LEV, SPLIT>(ga, tile, rec, lane, g, dmask);
+    uint32_t dmask = 0;
+    if constexpr (WHOLE) mean_grad_whole<T, LEV>(ga, tile, rec, lane, g);
+    else mean_grad_part<T, LEV>(ga, tile, rec, lane, g, dmask);
+    const float keep = rec.flags & kTileDecay ? a.keep : 1.f;
 
-    if constexpr (BITS == 8) {
+    float mn[8], vn[8], root[8];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < 2; ++q) {
+        if constexpr (BITS == 8) {
             const auto ma = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[q], false);
             const auto mb = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[q], true);
             const auto va = __builtin_amdgcn_cvt_pk_f32_fp8((int)vc[q], false);
@@ -116,85 +139,106 @@ __global__ __launch_bounds__(kThreads) void k_adamw(GradArgs ga, StepArgs a, int
             m[q] = f32x4{ma[0] * ms[q], ma[1] * ms[q], mb[0] * ms[q], mb[1] * ms[q]};
             s[q] = f32x4{va[0] * vs[q], va[1] * vs[q], vb[0] * vs[q], vb[1] * vs[q]};
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int k = 4 * q + e;
+            const float gr = g[k] * clip;
+            mn[k] = fmaf(a.beta1, m[q][e], a.c1 * gr);
+            const float v0 = BITS == 32 ? s[q][e] : s[q][e] * s[q][e];
+            vn[k] = fmaf(a.beta2, v0, (a.c2 * gr) * gr);
+        }
     }
-
-    uint32_t mtop[2] = {0u, 0u}, stop[2] = {0u, 0u};
+    roots(vn, root);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float gr = g[4 * q + e] * clip;
-            const float mn = fmaf(a.beta1, m[q][e], a.c1 * gr);
-            const float v0 = BITS == 32 ? s[q][e] : s[q][e] * s[q][e];
-            const float vn = fmaf(a.beta2, v0, (a.c2 * gr) * gr);
-            const float root = sqrtf(vn);
-            const float keep = (dmask >> (4 * q + e)) & 1u ? a.keep : 1.f;
-            w[q][e] = fmaf(-a.lr_t, mn / fmaf(root, a.rbc2, a.eps), w[q][e] * keep);
-            m[q][e] = mn;
-            if constexpr (BITS == 32) {
-                s[q][e] = vn;
-            } else {
-                const bool in = at[q] + e < ga.P;
-                s[q][e] = in ? root : 0.f;
-                m[q][e] = in ? mn : 0.f;
-                const uint32_t ma = __float_as_uint(m[q][e]) & 0x7fffffffu, sa = __float_as_uint(s[q][e]) & 0x7fffffffu;
-                mtop[q] = mtop[q] > ma ? mtop[q] : ma;
-                stop[q] = stop[q] > sa ? stop[q] : sa;
-            }
+            const int k = 4 * q + e;
+            // the hardware reciprocal is within 1 ulp of 1/x for the denominators there are: eps is 0 or
+            // normal, and the root of the least v is 2^-74.5
+            const float up = mn[k] * __builtin_amdgcn_rcpf(fmaf(root[k], a.rbc2, a.eps));
+            const float kp = WHOLE ? keep : (dmask >> k) & 1u ? a.keep : 1.f;
+            w[q][e] = fmaf(-a.lr_t, up, w[q][e] * kp);
+            if (BITS == 8 && !WHOLE && at[q] + e >= P) root[k] = mn[k] = 0.f;
         }
-        store4(a.w, at[q], ga.P, w[q]);
+        store4<WHOLE>(a.w + e0, at[q], P, w[q]);
         if (a.copy) {
-            if (a.copy_dtype == kB16) store4_narrow<kB16>(a.copy, at[q], ga.P, w[q]);
-            else store4_narrow<kF16>(a.copy, at[q], ga.P, w[q]);
+            if (a.copy_dtype == kB16) store4_narrow<kB16, WHOLE>(a.copy, e0, at[q], P, w[q]);
+            else store4_narrow<kF16, WHOLE>(a.copy, e0, at[q], P, w[q]);
         }
         if constexpr (BITS == 32) {
-            store4(static_cast<float*>(a.m), at[q], ga.P, m[q]);
-            store4(static_cast<float*>(a.v), at[q], ga.P, s[q]);
+            store4<WHOLE>(static_cast<float*>(a.m) + e0, at[q], P, f32x4{mn[4 * q], mn[4 * q + 1], mn[4 * q + 2], mn[4 * q + 3]});
+            store4<WHOLE>(static_cast<float*>(a.v) + e0, at[q], P, f32x4{vn[4 * q], vn[4 * q + 1], vn[4 * q + 2], vn[4 * q + 3]});
         }
     }
     if constexpr (BITS == 8) {
-        // the block's largest magnitudes (as bit patterns: a NaN wins), in every lane of the block
-        if constexpr (SPLIT) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                mtop[q] = wave_max_u32(mtop[q]);
-                stop[q] = wave_max_u32(stop[q]);
-            }
-        } else {
-            mtop[0] = mtop[1] = half_max_u32(mtop[0] > mtop[1] ? mtop[0] : mtop[1]);
-            stop[0] = stop[1] = half_max_u32(stop[0] > stop[1] ? stop[0] : stop[1]);
-        }
+        // The four block maxima (as bit patterns: a NaN wins) in one reduction: the halves of the wavefront take a
+        // block each, then the even and odd rows of 16 lanes m and the root; row 0 ends with m of block 0, row 1
+        // with its root, rows 2 and 3 with those of block 1.
+        uint32_t top[2][2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const float mt = __uint_as_float(mtop[q] > kFloorBits ? mtop[q] : kFloorBits);
-            const float st = __uint_as_float(stop[q] > kFloorBits ? stop[q] : kFloorBits);
-            const float mu = kCodeMax / mt, su = kCodeMax / st;
-            const uint32_t pair = (uint32_t)(at[q] >> 1) + a.seed;
-            const uint32_t rnd[2] = {mix(pair), mix(pair + 1u)};
-            float x[4];
+            top[0][q] = top[1][q] = 0u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float y = s[q][e] * su;
-                y = y > kCodeMax ? kCodeMax : y;
-                y = s[q][e] > 0.f && y < 0x1p-6f ? 0x1p-6f : y;
-                // 3 mantissa bits stay: 16 random bits, centred, on top of the 20 that go
-                const uint32_t r = e & 1 ? rnd[e >> 1] >> 16 : rnd[e >> 1] & 0xffffu;
-                x[e] = __uint_as_float((__float_as_uint(y) + ((r << 4) | 8u)) & 0xfff00000u);
+                const uint32_t ma = __float_as_uint(mn[4 * q + e]) & 0x7fffffffu;
+                const uint32_t sa = __float_as_uint(root[4 * q + e]) & 0x7fffffffu;
+                top[0][q] = top[0][q] > ma ? top[0][q] : ma;
+                top[1][q] = top[1][q] > sa ? top[1][q] : sa;
             }
-            int cv = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
-            cv = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], cv, true);
-            int cm = __builtin_amdgcn_cvt_pk_fp8_f32(m[q][0] * mu, m[q][1] * mu, 0, false);
-            cm = __builtin_amdgcn_cvt_pk_fp8_f32(m[q][2] * mu, m[q][3] * mu, cm, true);
-            if (at[q] < n_coded) {
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at[q]) = (uint32_t)cm;
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at[q]) = (uint32_t)cv;
-                if (at[q] % GA_STATE_BLOCK == 0) {
-                    a.m_scale[at[q] / GA_STATE_BLOCK] = mt * (1.f / kCodeMax);
-                    a.v_scale[at[q] / GA_STATE_BLOCK] = st * (1.f / kCodeMax);
-                }
+        }
+        const auto larger = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+        uint32_t half[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const auto r = __builtin_amdgcn_permlane32_swap(top[j][0], top[j][1], false, false);
+            half[j] = larger(r[0], r[1]);
+        }
+        const auto r16 = __builtin_amdgcn_permlane16_swap(half[0], half[1], false, false);
+        uint32_t row = reduce16(larger(r16[0], r16[1]), larger);
+        row = larger(row, kFloorBits);
+        const float largest = __uint_as_float(row);
+        const float unit = kCodeMax / largest;
+        if ((lane & 15) == 0 && (WHOLE || (lane >> 5) * GA_STATE_BLOCK < P))
+            (lane & 16 ? a.v_scale : a.m_scale)[tile * 2 + (lane >> 5)] = largest * (1.f / kCodeMax);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float mu = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(unit), 32 * q));
+            const float su = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(unit), 32 * q + 16));
+            const uint32_t pair = (uint32_t)((uint64_t)e0 >> 1) + a.seed + (uint32_t)(at[q] >> 1);
+            const uint32_t rnd[2] = {mix(pair), mix(pair + 1u)};
+            int cv = 0;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = root[4 * q + e];
+                y[e] = __builtin_amdgcn_fmed3f(x * su, 0x1p-6f, kCodeMax);
+                y[e] = x > 0.f ? y[e] : x;   // 0 stays 0, NaN stays NaN
+            }
+            // rounded by adding 20 random bits (16 of them, centred) to the 20 mantissa bits that go: the hardware's
+            // stochastic conversion adds the upper 20 bits of its second operand
+            cv = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], (rnd[0] << 16) | 0x8000u, cv, 0);
+            cv = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (rnd[0] & 0xffff0000u) | 0x8000u, cv, 1);
+            cv = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (rnd[1] << 16) | 0x8000u, cv, 2);
+            cv = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], (rnd[1] & 0xffff0000u) | 0x8000u, cv, 3);
+            int cm = __builtin_amdgcn_cvt_pk_fp8_f32(mn[4 * q] * mu, mn[4 * q + 1] * mu, 0, false);
+            cm = __builtin_amdgcn_cvt_pk_fp8_f32(mn[4 * q + 2] * mu, mn[4 * q + 3] * mu, cm, true);
+            if (WHOLE || q * GA_STATE_BLOCK < P) {
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + e0 + at[q]) = (uint32_t)cm;
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + e0 + at[q]) = (uint32_t)cv;
             }
         }
     }
+}
+
+template <int T, int BITS, int LEV>
+__global__ __launch_bounds__(kThreads) void k_adamw(GradArgs ga, StepArgs a, int64_t n_tiles) {
+    const int lane = threadIdx.x & 63;
+    const int64_t tile = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (tile >= n_tiles) return;
+    const TileRec rec = ga.tiles[tile];
+    if (rec.flags & kTileWhole) adamw_tile<T, BITS, LEV, true>(ga, a, tile, rec, lane);
+    else adamw_tile<T, BITS, LEV, false>(ga, a, tile, rec, lane);
 }
 
 template <int T, int BITS>
@@ -202,7 +246,7 @@ hipError_t adamw_launch(const Adamw& o, const uint64_t* layer_ptrs, const StepAr
     const GradArgs g = grad_args(o, layer_ptrs);
     const unsigned blocks = (unsigned)((o.n_tiles + kThreads / 64 - 1) / (kThreads / 64));
     return with_levels(o.W, [&](auto lev) {
-        hipLaunchKernelGGL((k_adamw<T, BITS, decltype(lev)::value, false>), dim3(blocks), dim3(kThreads), 0, s, g, a,
+        hipLaunchKernelGGL((k_adamw<T, BITS, decltype(lev)::value>), dim3(blocks), dim3(kThreads), 0, s, g, a,
                            o.n_tiles);
         return hipGetLastError();
     });

@@ -150,18 +150,18 @@ __device__ __forceinline__ uint32_t lane_move(uint32_t x) {
 }
 
 template <typename OP>
-__device__ __forceinline__ uint32_t reduce32(uint32_t x, OP op) {
+__device__ __forceinline__ uint32_t reduce16(uint32_t x, OP op) {
     x = op(x, lane_move<0xb1>(x));    // xor 1
     x = op(x, lane_move<0x4e>(x));    // xor 2
     x = op(x, lane_move<0x141>(x));   // mirror within 8
-    x = op(x, lane_move<0x140>(x));   // mirror within 16
-    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    return op(r[0], r[1]);
+    return op(x, lane_move<0x140>(x));   // mirror within 16
 }
 
 template <typename OP>
 __device__ __forceinline__ uint32_t reduce64(uint32_t x, OP op) {
-    x = reduce32(x, op);
+    x = reduce16(x, op);
+    const auto r16 = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = op(r16[0], r16[1]);
     const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
     return op(r[0], r[1]);
 }
@@ -170,16 +170,6 @@ __device__ __forceinline__ float wave_sum_f32(float x) {
     return __uint_as_float(reduce64(__float_as_uint(x), [](uint32_t a, uint32_t b) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
-}
-
-// Largest of the lanes' bit patterns: for magnitudes this is the largest
-// value, and a NaN wins.
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
-    return reduce64(x, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-}
-
-__device__ __forceinline__ uint32_t half_max_u32(uint32_t x) {
-    return reduce32(x, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
 __device__ __forceinline__ double wave_sum_f64(double x) {

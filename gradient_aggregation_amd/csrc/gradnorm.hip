@@ -13,7 +13,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kEndThreads = 1024;
 
-template <int T, int LEV, bool SPLIT>
+template <int T, int LEV>
 __global__ __launch_bounds__(kThreads) void k_grad_norm(GradArgs a, int64_t n_tiles, float* __restrict__ grad,
                                                         double* __restrict__ partials) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -23,7 +23,8 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(GradArgs a, int64_t n_ti
         const TileRec rec = a.tiles[tile];
         float g[8];
         uint32_t dmask;
-        mean_grad<T, LEV, SPLIT>(a, tile, rec, lane, g, dmask);
+        if (rec.flags & kTileWhole) mean_grad_whole<T, LEV>(a, tile, rec, lane, g);
+        else mean_grad_part<T, LEV>(a, tile, rec, lane, g, dmask);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             acc0 = fma((double)g[e], (double)g[e], acc0);
@@ -32,7 +33,7 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(GradArgs a, int64_t n_ti
         if (grad) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t i = group_at<SPLIT>(tile, lane, q);
+                const int64_t i = group_at(tile, lane, q);
                 if (i + 4 <= a.P) {
                     __builtin_nontemporal_store(f32x4{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]},
                                                 reinterpret_cast<f32x4*>(grad + i));
@@ -77,7 +78,7 @@ hipError_t norm_launch(const Adamw& o, const uint64_t* layer_ptrs, float max_nor
     const int64_t want = (o.n_tiles + kThreads / 64 - 1) / (kThreads / 64);
     const int32_t blocks = (int32_t)(want < kNormBlocks ? want : kNormBlocks);
     const hipError_t e = with_levels(o.W, [&](auto lev) {
-        hipLaunchKernelGGL((k_grad_norm<T, decltype(lev)::value, false>), dim3(blocks), dim3(kThreads), 0, s, g,
+        hipLaunchKernelGGL((k_grad_norm<T, decltype(lev)::value>), dim3(blocks), dim3(kThreads), 0, s, g,
                            o.n_tiles, grad, o.d_partials);
         return hipGetLastError();
     });

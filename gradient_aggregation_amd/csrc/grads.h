@@ -21,161 +21,172 @@ struct GradArgs {
     float inv_w;
 };
 
-// A lane's 8 elements are two groups of 4: with SPLIT the groups lie 256
-// elements apart, so that a wavefront's 128-bit accesses to binary32 vectors
-// are one contiguous run; without it they are neighbours, so that 8 16-bit
-// elements are one 128-bit access.
-template <bool SPLIT>
-__device__ __forceinline__ int64_t group_at(int64_t tile, int lane, int q) {
-    return tile * kTile + (SPLIT ? q * 256 + lane * 4 : lane * 8 + q * 4);
-}
-
-template <int T, bool SPLIT>
-__device__ __forceinline__ void load_leaf8(Raw<T, 8>& x, uint64_t addr) {
-    if constexpr (SPLIT) {
-        Raw<T, 4> a, b;
-        a.template load<true>(addr);
-        b.template load<true>(addr + 256 * kSize<T>);
-#pragma unroll
-        for (int j = 0; j < Raw<T, 4>::WORDS; ++j) {
-            x.w[j] = a.w[j];
-            x.w[Raw<T, 4>::WORDS + j] = b.w[j];
-        }
-    } else {
-        x.template load<true>(addr);
-    }
-}
+// A lane's 8 elements are two groups of 4, 256 elements apart: each of a
+// wavefront's accesses, to a gradient as to a binary32 vector, is one run with
+// no gaps.  (With the groups side by side a wavefront's binary32 access is
+// every other 16 bytes of its run, each 128-byte line is asked for twice, and
+// streaming hints make the second time a miss: the update of 7.6M parameters
+// took 94 us that way.)
+__device__ __forceinline__ int64_t group_at(int64_t tile, int lane, int q) { return tile * kTile + q * 256 + lane * 4; }
 
 // Leaves in flight per lane and levels of the tree for W workers, W < 2^LEV.
 template <int LEV>
 constexpr int kInFlight = LEV <= 1 ? 1 : LEV <= 3 ? 4 : LEV <= 8 ? 8 : 4;
 
-// g[4q + e] = the mean gradient of element group_at(q) + e (0 past P); bit
-// 4q + e of dmask: the element's layer decays.  All 64 lanes take part.
-template <int T, int LEV, bool SPLIT>
-__device__ __forceinline__ void mean_grad(const GradArgs& a, int64_t tile, const TileRec& rec, int lane, float (&g)[8],
-                                          uint32_t& dmask) {
-    constexpr int SZ = kSize<T>;
-    constexpr int U = kInFlight<LEV>;
-    TreeAcc<LEV, 8> tree;
-    uint32_t cnt = 0;
-    if (rec.flags & kTileWhole) {
-        dmask = rec.flags & kTileDecay ? 0xffu : 0u;
-        const uint64_t at = (uint64_t)((group_at<SPLIT>(tile, lane, 0) - rec.start) * SZ);
-        if constexpr (LEV == 1) {
-            Raw<T, 8> x;
-            load_leaf8<T, SPLIT>(x, a.ptrs[rec.layer] + at);
-            x.widen(g);
-            return;
-        } else {
-            for (int32_t g0 = 0; g0 < a.W; g0 += 64) {
-                // lane l holds worker (g0 + l)'s address, read out lane by lane
-                const int32_t gn = a.W - g0 < 64 ? a.W - g0 : 64;
-                const uint64_t mine = lane < gn ? a.ptrs[(int64_t)(g0 + lane) * a.L + rec.layer] : 0ull;
-                const int lo = (int)(uint32_t)mine, hi = (int)(uint32_t)(mine >> 32);
-                for (int32_t u0 = 0; u0 < gn; u0 += U) {
-                    Raw<T, 8> x[U];
+template <int T>
+struct Leaf {
+    Raw<T, 4> q0, q1;
+    __device__ __forceinline__ void load(uint64_t base, uint32_t at) {
+        q0.template load<true>(base + at);
+        q1.template load<true>(base + at + 256 * kSize<T>);
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+        float a[4], b[4];
+        q0.widen(a);
+        q1.widen(b);
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (u0 + u < gn) {
-                            const uint64_t base = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, u0 + u) << 32) |
-                                                  (uint32_t)__builtin_amdgcn_readlane(lo, u0 + u);
-                            load_leaf8<T, SPLIT>(x[u], base + at);
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (u0 + u < gn) {
-                            float f[8];
-                            x[u].widen(f);
-                            tree.push(f, cnt);
-                            ++cnt;
-                        }
-                    }
-                }
-            }
+        for (int e = 0; e < 4; ++e) {
+            f[e] = a[e];
+            f[4 + e] = b[e];
         }
+    }
+};
+
+// g[4q + e] = the mean gradient of element group_at(q) + e of a tile that lies
+// in one layer.  All 64 lanes take part; tile and rec are the wavefront's.
+template <int T, int LEV>
+__device__ __forceinline__ void mean_grad_whole(const GradArgs& a, int64_t tile, const TileRec& rec, int lane,
+                                                float (&g)[8]) {
+    const uint64_t in_layer = (uint64_t)(tile * kTile - rec.start) * kSize<T>;
+    const uint32_t at = (uint32_t)lane * 4 * kSize<T>;
+    if constexpr (LEV == 1) {
+        Leaf<T> x;
+        x.load(a.ptrs[rec.layer] + in_layer, at);
+        x.widen(g);
     } else {
-        // The tile straddles a layer boundary or holds the tail: each group
-        // resolves its own layer; one whose 4 elements lie in one layer is a
-        // vector load, the others go element by element.
-        constexpr int V = U < 4 ? U : 4;
-        int64_t i[2], start[2];
-        int32_t layer[2];
-        bool vec[2], part[2];
-        dmask = 0;
+        constexpr int U = kInFlight<LEV>;
+        TreeAcc<LEV, 8> tree;
+        uint32_t cnt = 0;
+        for (int32_t g0 = 0; g0 < a.W; g0 += 64) {
+            // lane l holds worker (g0 + l)'s address, read out lane by lane
+            const int32_t gn = a.W - g0 < 64 ? a.W - g0 : 64;
+            const uint64_t mine = lane < gn ? a.ptrs[(int64_t)(g0 + lane) * a.L + rec.layer] : 0ull;
+            const int lo = (int)(uint32_t)mine, hi = (int)(uint32_t)(mine >> 32);
+            for (int32_t u0 = 0; u0 < gn; u0 += U) {
+                Leaf<T> x[U];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            i[q] = group_at<SPLIT>(tile, lane, q);
-            int32_t lo = (int32_t)rec.layer, hi = a.L - 1;
-            while (lo < hi) {
-                const int32_t mid = (lo + hi) >> 1;
-                if (a.offsets[mid + 1] <= i[q]) lo = mid + 1;
-                else hi = mid;
-            }
-            layer[q] = lo;
-            start[q] = a.offsets[lo];
-            vec[q] = i[q] + 4 <= a.offsets[lo + 1];
-            part[q] = !vec[q] && i[q] < a.P;
-            if (vec[q]) {
-                dmask |= a.decay[lo] ? 0xfu << (4 * q) : 0u;
-            } else if (part[q]) {
-                int32_t l = lo;
-                for (int e = 0; e < 4 && i[q] + e < a.P; ++e) {
-                    while (a.offsets[l + 1] <= i[q] + e) ++l;
-                    dmask |= a.decay[l] ? 1u << (4 * q + e) : 0u;
-                }
-            }
-        }
-        for (int32_t w0 = 0; w0 < a.W; w0 += V) {
-            float f[V][8];
-#pragma unroll
-            for (int u = 0; u < V; ++u)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (vec[q]) {
-                    uint64_t base[V];
-                    Raw<T, 4> x[V];
-#pragma unroll
-                    for (int u = 0; u < V; ++u)
-                        base[u] = a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + layer[q]];
-#pragma unroll
-                    for (int u = 0; u < V; ++u) x[u].load(base[u] + (uint64_t)((i[q] - start[q]) * SZ));
-#pragma unroll
-                    for (int u = 0; u < V; ++u) {
-                        float h[4];
-                        x[u].widen(h);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[u][4 * q + e] = h[e];
-                    }
-                } else if (part[q]) {
-                    int32_t l = layer[q];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (i[q] + e < a.P) {
-                            while (a.offsets[l + 1] <= i[q] + e) ++l;
-                            const uint64_t at = (uint64_t)((i[q] + e - a.offsets[l]) * SZ);
-#pragma unroll
-                            for (int u = 0; u < V; ++u)
-                                f[u][4 * q + e] =
-                                    load_one<T>(a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + l] + at);
-                        }
+                for (int u = 0; u < U; ++u) {
+                    if (u0 + u < gn) {
+                        const uint64_t base = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, u0 + u) << 32) |
+                                              (uint32_t)__builtin_amdgcn_readlane(lo, u0 + u);
+                        x[u].load(base + in_layer, at);
                     }
                 }
-            }
-            if constexpr (LEV == 1) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = f[0][e];
-                return;
-            } else {
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    if (w0 + u < a.W) {
-                        tree.push(f[u], cnt);
+                for (int u = 0; u < U; ++u) {
+                    if (u0 + u < gn) {
+                        float f[8];
+                        x[u].widen(f);
+                        tree.push(f, cnt);
                         ++cnt;
                     }
+                }
+            }
+        }
+        float s[8];
+        tree.result((uint32_t)a.W, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = s[e] * a.inv_w;
+    }
+}
+
+// The same of a tile that straddles a layer boundary or holds the tail (0 past
+// P); bit 4q + e of dmask: the element's layer decays.  Each group resolves its
+// own layer, between those of the tile's first and last element; one whose 4
+// elements lie in one layer is a vector load, the others go element by element.
+template <int T, int LEV>
+__device__ __forceinline__ void mean_grad_part(const GradArgs& a, int64_t tile, const TileRec& rec, int lane,
+                                               float (&g)[8], uint32_t& dmask) {
+    constexpr int SZ = kSize<T>;
+    constexpr int V = kInFlight<LEV> < 4 ? kInFlight<LEV> : 4;
+    TreeAcc<LEV, 8> tree;
+    uint32_t cnt = 0;
+    int64_t i[2], start[2];
+    int32_t layer[2];
+    bool vec[2], part[2];
+    dmask = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        i[q] = group_at(tile, lane, q);
+        int32_t lo = (int32_t)rec.layer, hi = lo + (int32_t)(rec.flags >> kTileSpanShift);
+        if (hi > a.L - 1) hi = a.L - 1;
+        while (lo < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (a.offsets[mid + 1] <= i[q]) lo = mid + 1;
+            else hi = mid;
+        }
+        layer[q] = lo;
+        start[q] = a.offsets[lo];
+        vec[q] = i[q] + 4 <= a.offsets[lo + 1];
+        part[q] = !vec[q] && i[q] < a.P;
+        if (vec[q]) {
+            dmask |= a.decay[lo] ? 0xfu << (4 * q) : 0u;
+        } else if (part[q]) {
+            int32_t l = lo;
+            for (int e = 0; e < 4 && i[q] + e < a.P; ++e) {
+                while (a.offsets[l + 1] <= i[q] + e) ++l;
+                dmask |= a.decay[l] ? 1u << (4 * q + e) : 0u;
+            }
+        }
+    }
+    for (int32_t w0 = 0; w0 < a.W; w0 += V) {
+        float f[V][8];
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (vec[q]) {
+                uint64_t base[V];
+                Raw<T, 4> x[V];
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+                    base[u] = a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + layer[q]];
+#pragma unroll
+                for (int u = 0; u < V; ++u) x[u].load(base[u] + (uint64_t)((i[q] - start[q]) * SZ));
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    float h[4];
+                    x[u].widen(h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[u][4 * q + e] = h[e];
+                }
+            } else if (part[q]) {
+                int32_t l = layer[q];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (i[q] + e < a.P) {
+                        while (a.offsets[l + 1] <= i[q] + e) ++l;
+                        const uint64_t at = (uint64_t)((i[q] + e - a.offsets[l]) * SZ);
+#pragma unroll
+                        for (int u = 0; u < V; ++u)
+                            f[u][4 * q + e] =
+                                load_one<T>(a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + l] + at);
+                    }
+                }
+            }
+        }
+        if constexpr (LEV == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = f[0][e];
+            return;
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                if (w0 + u < a.W) {
+                    tree.push(f[u], cnt);
+                    ++cnt;
                 }
             }
         }

@@ -17,10 +17,11 @@ constexpr int kTile = 512;
 struct TileRec {
     int64_t start;      // first element of the layer
     uint32_t layer;
-    uint32_t flags;     // kTileWhole | kTileDecay
+    uint32_t flags;     // kTileWhole | kTileDecay | layers after this one in the tile << kTileSpanShift
 };
 constexpr uint32_t kTileWhole = 1u;   // all kTile elements exist and lie in this layer
 constexpr uint32_t kTileDecay = 2u;   // the layer's weights decay
+constexpr int kTileSpanShift = 16;    // a tile of 512 elements holds at most 512 layers
 
 // Workgroups of the norm pass at most: its partial sums are one binary64 each.
 constexpr int kNormBlocks = 2048;

@@ -94,7 +94,11 @@ ga_status ga_adamw_create(int32_t W, int32_t n_layers, const int64_t* layer_nume
         while (offs[l + 1] <= e0) ++l;
         tiles[t].start = offs[l];
         tiles[t].layer = (uint32_t)l;
-        tiles[t].flags = (offs[l + 1] >= e0 + ga::kTile ? ga::kTileWhole : 0u) | (flags[l] ? ga::kTileDecay : 0u);
+        const int64_t last = (e0 + ga::kTile < info.P ? e0 + ga::kTile : info.P) - 1;
+        int32_t end = l;
+        while (offs[end + 1] <= last) ++end;
+        tiles[t].flags = (offs[l + 1] >= e0 + ga::kTile ? ga::kTileWhole : 0u) | (flags[l] ? ga::kTileDecay : 0u) |
+                         ((uint32_t)(end - l) << ga::kTileSpanShift);
     }
     char* d = nullptr;
     hipError_t e = hipGetDevice(&o->device);
@@ -163,7 +167,8 @@ ga_status ga_adamw_step(const ga_adamw* opt, const uint64_t* d_layer_ptrs, const
     a.beta2 = params->beta2;
     a.c1 = (float)(1.0 - b1);
     a.c2 = (float)(1.0 - b2);
-    a.eps = params->eps;
+    // a denormal eps would have no reciprocal in the kernel's hardware instruction
+    a.eps = params->eps > 0.f && params->eps < 0x1p-126f ? 0x1p-126f : params->eps;
     a.rbc2 = (float)(1.0 / sqrt(1.0 - pow(b2, (double)params->t)));
     a.keep = (float)(1.0 - lr * (double)params->weight_decay);
     a.seed = (uint32_t)((uint64_t)params->t * 0x9E3779B9u + 0x7F4A7C15u);
