@@ -104,28 +104,33 @@ __device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a
     f32x4 w[2], m[2], s[2];   // s: v for binary32 moments, its root for codes
     float ms[2], vs[2];
     uint32_t mc[2], vc[2];
+    const auto load_state = [&] {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        w[q] = load4<WHOLE>(a.w + e0, at[q], P);
-        if constexpr (BITS == 32) {
-            m[q] = load4<WHOLE>(static_cast<const float*>(a.m) + e0, at[q], P);
-            s[q] = load4<WHOLE>(static_cast<const float*>(a.v) + e0, at[q], P);
-        } else {
-            mc[q] = vc[q] = 0u;
-            ms[q] = vs[q] = 0.f;
-            if (WHOLE || q * GA_STATE_BLOCK < P) {
-                mc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + e0 + at[q]);
-                vc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + e0 + at[q]);
-                ms[q] = a.m_scale[tile * 2 + q];
-                vs[q] = a.v_scale[tile * 2 + q];
+        for (int q = 0; q < 2; ++q) {
+            w[q] = load4<WHOLE>(a.w + e0, at[q], P);
+            if constexpr (BITS == 32) {
+                m[q] = load4<WHOLE>(static_cast<const float*>(a.m) + e0, at[q], P);
+                s[q] = load4<WHOLE>(static_cast<const float*>(a.v) + e0, at[q], P);
+            } else {
+                mc[q] = vc[q] = 0u;
+                ms[q] = vs[q] = 0.f;
+                if (WHOLE || q * GA_STATE_BLOCK < P) {
+                    mc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + e0 + at[q]);
+                    vc[q] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + e0 + at[q]);
+                    ms[q] = a.m_scale[tile * 2 + q];
+                    vs[q] = a.v_scale[tile * 2 + q];
+                }
             }
         }
-    }
-
+    };
+    // with several workers the leaves and their tree come first: the state's 24 registers beside them would cost a
+    // wavefront per SIMD (61M parameters of 16 workers: 642 us; 588 us at four per SIMD)
+    if constexpr (LEV == 1) load_state();
     float g[8];
     uint32_t dmask = 0;
     if constexpr (WHOLE) mean_grad_whole<T, LEV>(ga, tile, rec, lane, g);
     else mean_grad_part<T, LEV>(ga, tile, rec, lane, g, dmask);
+    if constexpr (LEV > 1) load_state();
     const float keep = rec.flags & kTileDecay ? a.keep : 1.f;
 
     float mn[8], vn[8], root[8];
@@ -231,8 +236,13 @@ __device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a
     }
 }
 
+// Wavefronts per SIMD that the registers are cut to (128 at 4): trees of up to
+// 5 levels fit without spilling, deeper ones do not.
+template <int LEV>
+constexpr int kWaves = LEV > 1 && LEV <= 5 ? 4 : 1;
+
 template <int T, int BITS, int LEV>
-__global__ __launch_bounds__(kThreads) void k_adamw(GradArgs ga, StepArgs a, int64_t n_tiles) {
+__global__ __launch_bounds__(kThreads, kWaves<LEV>) void k_adamw(GradArgs ga, StepArgs a, int64_t n_tiles) {
     const int lane = threadIdx.x & 63;
     const int64_t tile = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (tile >= n_tiles) return;
