@@ -34,7 +34,8 @@ struct Adamw {
     TileRec* d_tiles;
     int64_t* d_offsets;
     uint8_t* d_decay;
-    double* d_partials;   // [kNormBlocks]
+    double* d_partials;   // [kNormBlocks], then d_done
+    uint32_t* d_done;     // workgroups of a norm call that have ended; 0 between calls
 };
 
 struct StepArgs {

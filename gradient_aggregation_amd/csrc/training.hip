@@ -104,7 +104,11 @@ ga_status ga_adamw_create(int32_t W, int32_t n_layers, const int64_t* layer_nume
     hipError_t e = hipGetDevice(&o->device);
     if (e == hipSuccess) e = hipMalloc((void**)&d, all_b);
     if (e == hipSuccess) e = hipMemcpy(d, h, all_b, hipMemcpyHostToDevice);
-    if (e == hipSuccess) e = hipMalloc((void**)&o->d_partials, sizeof(double) * ga::kNormBlocks);
+    const size_t parts_b = sizeof(double) * ga::kNormBlocks;
+    const uint64_t zero = 0;
+    if (e == hipSuccess) e = hipMalloc((void**)&o->d_partials, parts_b + sizeof zero);
+    if (e == hipSuccess) e = hipMemcpy(o->d_partials + ga::kNormBlocks, &zero, sizeof zero, hipMemcpyHostToDevice);
+    o->d_done = reinterpret_cast<uint32_t*>(o->d_partials + ga::kNormBlocks);
     free(h);
     o->d_tiles = reinterpret_cast<ga::TileRec*>(d);
     if (e != hipSuccess) {
