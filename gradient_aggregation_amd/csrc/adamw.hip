@@ -68,11 +68,20 @@ __device__ __forceinline__ void store4_narrow(void* p, int64_t e0, int i, int64_
     }
 }
 
-// Square roots of 8 values >= 0.  The hardware instruction is within 1 ulp
-// (1.54 half steps over 2^20 values of every exponent) but takes denormal
-// values for zero, which only matters when one is there: then the small values
-// are scaled up by 2^64 and the roots back by 2^-32, both exact.
+// Square roots of 8 values >= 0.  EXACT: rounded correctly, for the roots that
+// are held as codes: a code is cut from the root's bits, and a root one ulp off
+// would now and then be the neighbouring code, a sixteenth away.  Else the
+// hardware instruction, within 1 ulp (1.54 half steps over 2^20 values of every
+// exponent).  It takes denormal values for zero, which only matters when one is
+// there: then the small values are scaled up by 2^64 and the roots back by
+// 2^-32, both exact.
+template <bool EXACT>
 __device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
+    if constexpr (EXACT) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = sqrtf(v[e]);
+        return;
+    }
     uint32_t low = __float_as_uint(v[0]);
 #pragma unroll
     for (int e = 1; e < 8; ++e) low = __float_as_uint(v[e]) < low ? __float_as_uint(v[e]) : low;
@@ -148,12 +157,12 @@ __device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a
         for (int e = 0; e < 4; ++e) {
             const int k = 4 * q + e;
             const float gr = g[k] * clip;
-            mn[k] = fmaf(a.beta1, m[q][e], a.c1 * gr);
+            mn[k] = a.beta1 * m[q][e] + a.c1 * gr;
             const float v0 = BITS == 32 ? s[q][e] : s[q][e] * s[q][e];
-            vn[k] = fmaf(a.beta2, v0, (a.c2 * gr) * gr);
+            vn[k] = a.beta2 * v0 + (a.c2 * gr) * gr;
         }
     }
-    roots(vn, root);
+    roots<BITS == 8>(vn, root);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
 #pragma unroll
@@ -203,7 +212,7 @@ __device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a
         uint32_t row = reduce16(larger(r16[0], r16[1]), larger);
         row = larger(row, kFloorBits);
         const float largest = __uint_as_float(row);
-        const float unit = kCodeMax / largest;
+        const float unit = (1.f / largest) * kCodeMax;
         if ((lane & 15) == 0 && (WHOLE || (lane >> 5) * GA_STATE_BLOCK < P))
             (lane & 16 ? a.v_scale : a.m_scale)[tile * 2 + (lane >> 5)] = largest * (1.f / kCodeMax);
 #pragma unroll
