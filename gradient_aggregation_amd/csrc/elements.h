@@ -157,19 +157,20 @@ __device__ __forceinline__ uint32_t reduce16(uint32_t x, OP op) {
     return op(x, lane_move<0x140>(x));   // mirror within 16
 }
 
-template <typename OP>
-__device__ __forceinline__ uint32_t reduce64(uint32_t x, OP op) {
-    x = reduce16(x, op);
-    const auto r16 = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    x = op(r16[0], r16[1]);
-    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    return op(r[0], r[1]);
-}
-
-__device__ __forceinline__ float wave_sum_f32(float x) {
-    return __uint_as_float(reduce64(__float_as_uint(x), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-    }));
+// Sum over aligned runs of T lanes (16, 32 or 64).
+template <int T>
+__device__ __forceinline__ float lanes_sum_f32(float x) {
+    const auto add = [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); };
+    uint32_t u = reduce16(__float_as_uint(x), add);
+    if constexpr (T >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        u = add(r[0], r[1]);
+    }
+    if constexpr (T >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        u = add(r[0], r[1]);
+    }
+    return __uint_as_float(u);
 }
 
 __device__ __forceinline__ double wave_sum_f64(double x) {

@@ -56,7 +56,7 @@ hipError_t launch_grad_norm(const Adamw& o, const uint64_t* layer_ptrs, float ma
 hipError_t launch_adamw(const Adamw& o, const uint64_t* layer_ptrs, const StepArgs& a, hipStream_t s);
 
 // Partial rows of the weight gradients at most (all groups together).
-constexpr int kLnParts = 512;
+constexpr int kLnParts = 256;
 
 struct LayerNorm {
     int64_t dim, ldp;      // ldp: stride of a partial row (dim rounded up to 4)

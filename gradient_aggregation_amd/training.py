@@ -158,7 +158,7 @@ def _rows(t, like, name: str):
 class LayerNorm:
     """Layer norm over the last dimension (`dim` elements of x_dtype), weight and
     bias of p_dtype (float32 or x_dtype).  backward=False makes a handle without
-    the backward pass's workspace (4096 * dim bytes)."""
+    the backward pass's workspace (2048 * dim bytes)."""
 
     def __init__(self, dim: int, x_dtype=torch.float32, p_dtype=torch.float32, backward: bool = True):
         xd, pd = _dtype(x_dtype, "x_dtype"), _dtype(p_dtype, "p_dtype")

@@ -599,8 +599,8 @@ typedef struct ga_layernorm ga_layernorm;
 /*
  * Layer norm over rows of dim elements of x_dtype, with weight and bias
  * vectors of p_dtype (GA_FP32 or x_dtype), on the current device.  The handle
- * owns the workspace of the backward pass's weight gradients: 512 partial rows
- * of each, 4096 * (dim rounded up to 4) bytes, unless backward == 0 (then
+ * owns the workspace of the backward pass's weight gradients: 256 partial rows
+ * of each, 2048 * (dim rounded up to 4) bytes, unless backward == 0 (then
  * ga_layernorm_backward refuses the handle).
  * GA_ERR_INVALID: dim < 1 or a type that is not listed; GA_ERR_UNSUPPORTED:
  * dim > GA_MAX_DIM.
