@@ -206,15 +206,17 @@ def _torch():
 
 
 def _stream_ptr() -> int:
-    return _torch().cuda.current_stream().cuda_stream
+    """The current stream of the current device (without the stream object that
+    torch.cuda.current_stream() makes: 0.2 against 2.6 us)."""
+    C = _torch()._C
+    return C._cuda_getCurrentRawStream(C._cuda_getDevice())
 
 
 def _dev(t, dtype, min_numel: int, name: str):
     """Address of a contiguous CUDA tensor of `dtype` with at least min_numel elements."""
-    torch = _torch()
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
