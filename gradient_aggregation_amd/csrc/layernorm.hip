@@ -60,6 +60,48 @@ __device__ __forceinline__ void load_part(Raw<X, N>& r, uint64_t row, int64_t c,
     r.narrow(f);
 }
 
+// The same in two steps, for rows read ahead: the load itself, in which the
+// vector that would pass the end is read from where it ends there instead (a
+// load per element would have to be waited for at once), and the shift that
+// moves its elements into place and fills up with zeros.
+template <int X, int N, bool NT>
+__device__ __forceinline__ void load_ahead(Raw<X, N>& r, uint64_t row, int32_t c, int32_t dim) {
+    if (dim < N) {
+        load_part(r, row, c, dim);
+    } else if (c < dim) {
+        r.template load<NT>(row + (uint64_t)((c < dim - N ? c : dim - N) * kSize<X>));
+    } else {
+#pragma unroll
+        for (int j = 0; j < Raw<X, N>::WORDS; ++j) r.w[j] = 0u;
+    }
+}
+
+template <int X, int N>
+__device__ __forceinline__ void into_place(Raw<X, N>& r, int32_t c, int32_t dim) {
+    static_assert(Raw<X, N>::WORDS == 4, "a 128-bit vector");
+    if (dim < N || dim % N == 0) return;
+    const int past = c + N - dim;
+    const uint32_t s = past > 0 && past < N ? past : 0;   // elements to drop
+    const uint32_t words = s * kSize<X> / 4;
+    if (words & 2u) {
+        r.w[0] = r.w[2];
+        r.w[1] = r.w[3];
+        r.w[2] = r.w[3] = 0u;
+    }
+    if (words & 1u) {
+        r.w[0] = r.w[1];
+        r.w[1] = r.w[2];
+        r.w[2] = r.w[3];
+        r.w[3] = 0u;
+    }
+    if (kSize<X> == 2 && (s & 1u)) {
+        r.w[0] = __builtin_amdgcn_alignbit(r.w[1], r.w[0], 16);
+        r.w[1] = __builtin_amdgcn_alignbit(r.w[2], r.w[1], 16);
+        r.w[2] = __builtin_amdgcn_alignbit(r.w[3], r.w[2], 16);
+        r.w[3] >>= 16;
+    }
+}
+
 template <int X, bool NT = false, int N>
 __device__ __forceinline__ void store_part(const float (&f)[N], uint64_t row, int64_t c, int64_t dim) {
     const uint64_t at = row + (uint64_t)c * kSize<X>;
@@ -130,10 +172,10 @@ __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim
             const int c = (v * T + t) * N;
             const uint64_t at = reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx);
             if (a.res) {
-                load_part<X, N, true>(x[v], at, c, dim);
-                load_part<X, N, true>(r[v], reinterpret_cast<uint64_t>(a.res) + (uint64_t)(row * a.ldr), c, dim);
+                load_ahead<X, N, true>(x[v], at, c, dim);
+                load_ahead<X, N, true>(r[v], reinterpret_cast<uint64_t>(a.res) + (uint64_t)(row * a.ldr), c, dim);
             } else {
-                load_part(x[v], at, c, dim);
+                load_ahead<X, N, false>(x[v], at, c, dim);
             }
         }
     };
@@ -149,9 +191,11 @@ __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim
         float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            into_place(x[v], (v * T + t) * N, dim);
             x[v].widen(f[v]);
             if (a.res) {
                 float h[N];
+                into_place(r[v], (v * T + t) * N, dim);
                 r[v].widen(h);
                 // the sum is rounded to x's type, as it is stored, before it is normalised
 #pragma unroll
@@ -159,9 +203,6 @@ __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim
                 Raw<X, N> s;
                 s.narrow(f[v]);
                 s.widen(f[v]);
-                if (a.sum)
-                    store_part<X, true>(f[v], reinterpret_cast<uint64_t>(a.sum) + (uint64_t)(row * a.lds),
-                                        (v * T + t) * N, dim);
             }
 #pragma unroll
             for (int e = 0; e < N; ++e) sum += f[v][e];
@@ -169,6 +210,13 @@ __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim
         const int64_t next = row + (int64_t)gridDim.x * R;
         if (next < a.rows) load_row(next);
         const float mean = team_sum<T>(sum, red[0]) * inv_dim;
+        // only now has the whole team read the row, which the sum may overwrite
+        if (a.sum) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                store_part<X, true>(f[v], reinterpret_cast<uint64_t>(a.sum) + (uint64_t)(row * a.lds), (v * T + t) * N,
+                                    dim);
+        }
         float sq = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -306,10 +354,10 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_bwd(LnBwd a, int32_t dim, in
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * T + t) * N;
-            load_part<X, N, true>(r.x[v], reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx), c, dim);
-            load_part<X, N, true>(r.dy[v], reinterpret_cast<uint64_t>(a.dy) + (uint64_t)(row * a.ldy), c, dim);
+            load_ahead<X, N, true>(r.x[v], reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx), c, dim);
+            load_ahead<X, N, true>(r.dy[v], reinterpret_cast<uint64_t>(a.dy) + (uint64_t)(row * a.ldy), c, dim);
             if (a.dsum)
-                load_part<X, N, true>(r.ds[v], reinterpret_cast<uint64_t>(a.dsum) + (uint64_t)(row * a.lds), c, dim);
+                load_ahead<X, N, true>(r.ds[v], reinterpret_cast<uint64_t>(a.dsum) + (uint64_t)(row * a.lds), c, dim);
         }
     };
     Row next;
@@ -338,6 +386,9 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_bwd(LnBwd a, int32_t dim, in
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float x[N], dy[N], gamma[N];
+                into_place(now.x[v], (v * T + t) * N, dim);
+                into_place(now.dy[v], (v * T + t) * N, dim);
+                if (a.dsum) into_place(now.ds[v], (v * T + t) * N, dim);
                 now.x[v].widen(x);
                 now.dy[v].widen(dy);
                 if constexpr (!HOLD) load_param<P>(gamma, a.gamma, (v * T + t) * N, dim, 1.f);
