@@ -7,8 +7,7 @@
 // nothing.  Backward: one pass over the rows as well; each thread keeps the
 // weight and the two weight-gradient sums of its columns in registers over all
 // the rows its workgroup takes, and the workgroup writes them as one partial row
-// at the end.  A second kernel adds the partial rows of each group in a fixed
-// order.
+// at the end.  The partial rows of each group are added in a fixed order.
 //
 // Bound by memory: b * (2 to 4) bytes per element forward, b * (3 to 4)
 // backward, against some 15 to 25 instructions.  16384 x 4096 bf16 rows: 94 us
@@ -330,7 +329,7 @@ __device__ __forceinline__ void store_param(void* out, int32_t dtype, int64_t i,
 // registers of its binary32 values.
 template <int X, int P, int T, int V>
 __global__ __launch_bounds__(kBwdThreads) void k_ln_bwd(LnBwd a, int32_t dim, int64_t ldp, int32_t parts,
-                                                        float* __restrict__ out) {
+                                                        float* out, uint32_t* done) {
     constexpr int N = kVec<X>, R = kBwdThreads / T, WAVES = T <= 64 ? 1 : T / 64;
     // 128 registers hold the next row beside one of 8 elements per thread.  Of 16 per thread, a wavefront's row
     // keeps the weight (60000 x 768 bf16 rows: 72 us; 92 reading it again), the widest rows not even that.
@@ -478,6 +477,40 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_bwd(LnBwd a, int32_t dim, in
                 put(1, c, db[v][e]);
             }
         }
+    }
+    if (!done) return;
+    // few partial rows: the group's workgroup that ends last adds them, in their order
+    __shared__ uint32_t last;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(done + group, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
+               (uint32_t)parts;
+    __syncthreads();
+    if (!last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    if (threadIdx.x == 0) __hip_atomic_store(done + group, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const float* p = out + (int64_t)group * parts * 2 * ldp;
+    for (int c = threadIdx.x * 4; c < 2 * (int)ldp; c += kBwdThreads * 4) {
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        for (int32_t k0 = 0; k0 < parts; k0 += 8) {
+            f32x4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = *reinterpret_cast<const f32x4*>(p + (int64_t)(k0 + k < parts ? k0 + k : parts - 1) * 2 * ldp + c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (k0 + k < parts) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] += x[k][e];
+                }
+            }
+        }
+        // ldp is a multiple of 4: the four columns are all of one gradient
+        void* g = c < (int)ldp ? a.dgamma : a.dbeta;
+        const int col = c < (int)ldp ? c : c - (int)ldp;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < dim) store_param(g, a.dp_dtype, (int64_t)group * dim + col + e, s[e]);
     }
 }
 
@@ -670,9 +703,17 @@ inline int32_t parts_of(const LnBwd& a, int rows_at_once) {
     return p < 1 ? 1 : (int32_t)p;
 }
 
+// Up to this many elements in a group's partial rows of one gradient, its
+// workgroup that ends last adds them itself; above, a second kernel does, which
+// costs a launch but spreads the sums over the chip.  Calls one after the other:
+// 8.4 against 10.4 us at 8192 (128 x 512 binary32 rows), 10.8 both ways at 12288
+// (256 x 768 bf16), 13.0 against 10.8 at 32768 (512 x 512).
+constexpr int64_t kOneLaunch = 12288;
+
 template <int X, int P>
 hipError_t ln_bwd(const LayerNorm& n, const LnBwd& a, hipStream_t s) {
     int32_t parts = 0;
+    bool one = false;
     hipError_t e = hipSuccess;
     if (a.rows > 0 && n.dim > kInRegisters) {
         if (a.dgamma) {
@@ -689,12 +730,13 @@ hipError_t ln_bwd(const LayerNorm& n, const LnBwd& a, hipStream_t s) {
         e = with_bwd_team<X>(n.dim, [&](auto t, auto v) {
             constexpr int T = decltype(t)::value, V = decltype(v)::value;
             parts = parts_of(a, kBwdThreads / T);
+            one = parts > 1 && parts * n.dim <= kOneLaunch;
             hipLaunchKernelGGL((k_ln_bwd<X, P, T, V>), dim3((unsigned)(a.groups * parts)), dim3(kBwdThreads), 0, s,
-                               a, (int32_t)n.dim, n.ldp, parts, n.d_parts);
+                               a, (int32_t)n.dim, n.ldp, parts, n.d_parts, one ? n.d_done : nullptr);
             return hipGetLastError();
         });
     }
-    if (e != hipSuccess || !a.dgamma || parts == 1) return e;
+    if (e != hipSuccess || !a.dgamma || parts == 1 || one) return e;
     hipLaunchKernelGGL(k_ln_params_end, dim3((unsigned)((2 * n.ldp + 63) / 64), (unsigned)a.groups), dim3(256), 0, s,
                        n.d_parts, n.dim, n.ldp, parts, a.dgamma, a.dbeta, a.dp_dtype);
     return hipGetLastError();

@@ -62,7 +62,8 @@ struct LayerNorm {
     int64_t dim, ldp;      // ldp: stride of a partial row (dim rounded up to 4)
     int32_t x_dtype, p_dtype;
     int device;
-    float* d_parts;        // [kLnParts][2][ldp], or nullptr
+    float* d_parts;        // [kLnParts][2][ldp], then d_done; or nullptr
+    uint32_t* d_done;      // [kLnParts] a group's workgroups that have ended; 0 between calls
 };
 
 struct LnFwd {

@@ -202,13 +202,20 @@ ga_status ga_layernorm_create(int64_t dim, ga_dtype x_dtype, ga_dtype p_dtype, i
     n->x_dtype = (int32_t)x_dtype;
     n->p_dtype = (int32_t)p_dtype;
     n->d_parts = nullptr;
+    n->d_done = nullptr;
     hipError_t e = hipGetDevice(&n->device);
-    if (e == hipSuccess && backward)
-        e = hipMalloc((void**)&n->d_parts, sizeof(float) * (size_t)ga::kLnParts * 2 * (size_t)n->ldp);
+    if (e == hipSuccess && backward) {
+        const size_t parts_b = sizeof(float) * (size_t)ga::kLnParts * 2 * (size_t)n->ldp;
+        const uint32_t zeros[ga::kLnParts] = {};
+        e = hipMalloc((void**)&n->d_parts, parts_b + sizeof zeros);
+        n->d_done = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(n->d_parts) + parts_b);
+        if (e == hipSuccess) e = hipMemcpy(n->d_done, zeros, sizeof zeros, hipMemcpyHostToDevice);
+    }
     if (e != hipSuccess) {
+        const ga_status bad = ga::api_fail(GA_ERR_DEVICE, hipGetErrorString(e));
         (void)hipGetLastError();
-        delete n;
-        return ga::api_fail(GA_ERR_DEVICE, hipGetErrorString(e));
+        ga_layernorm_destroy(reinterpret_cast<ga_layernorm*>(n));
+        return bad;
     }
     *out = reinterpret_cast<ga_layernorm*>(n);
     return ga::api_ok();
