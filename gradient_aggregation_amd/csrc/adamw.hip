@@ -102,9 +102,8 @@ __device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
 
 // One tile.  WHOLE: it lies in one layer and inside P.
 template <int T, int BITS, int LEV, bool WHOLE>
-__device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a, int64_t tile, const TileRec& rec,
-                                           int lane) {
-    const int64_t e0 = tile * kTile;
+__device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a, const TileRec& rec, int lane) {
+    const int64_t tile = rec.tile, e0 = tile * kTile;
     const int at[2] = {lane * 4, 256 + lane * 4};   // from e0
     const int64_t P = WHOLE ? (int64_t)kTile : ga.P - e0;
     float clip = 1.f;
@@ -248,19 +247,19 @@ __device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a
     }
 }
 
-// Wavefronts per SIMD that the registers are cut to (128 at 4): trees of up to
-// 5 levels fit without spilling, deeper ones do not.
+// Wavefronts per SIMD that the registers have to leave room for: trees of up to
+// 8 levels fit the 128 registers of 4, deeper ones spill some.
 template <int LEV>
-constexpr int kWaves = LEV > 1 && LEV <= 5 ? 4 : 1;
+constexpr int kWaves = LEV > 1 && LEV <= 8 ? 4 : 1;
 
 template <int T, int BITS, int LEV>
 __global__ __launch_bounds__(kThreads, kWaves<LEV>) void k_adamw(GradArgs ga, StepArgs a, int64_t n_tiles) {
     const int lane = threadIdx.x & 63;
-    const int64_t tile = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (tile >= n_tiles) return;
-    const TileRec rec = ga.tiles[tile];
-    if (rec.flags & kTileWhole) adamw_tile<T, BITS, LEV, true>(ga, a, tile, rec, lane);
-    else adamw_tile<T, BITS, LEV, false>(ga, a, tile, rec, lane);
+    const int64_t slot = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (slot >= n_tiles) return;
+    const TileRec rec = ga.tiles[slot];
+    if (rec.flags & kTileWhole) adamw_tile<T, BITS, LEV, true>(ga, a, rec, lane);
+    else adamw_tile<T, BITS, LEV, false>(ga, a, rec, lane);
 }
 
 template <int T, int BITS>

@@ -4,7 +4,8 @@
 // of squares per workgroup (each square is exact in binary64); they are added
 // in a fixed order, which forms the clip record.  Bound by memory: W * b bytes
 // per element, 4 more where the mean gradient is kept.  122 MB of bf16 gradients
-// take 23 us (5.3 TB/s) and the second kernel 4 us.  A wavefront takes one tile
+// take 22 us (5.5 TB/s) and the second kernel 4 us; 20M of 16 binary16 workers
+// 128 us with it (172 when the tiles that straddle layers came in turn).  A wavefront takes one tile
 // at a time: 2, 4 or 8 read together took 23 to 34 us, on 512 to 16384
 // workgroups, next to each other or a grid apart.
 #include "grads.h"
@@ -51,9 +52,10 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(GradArgs a, int64_t n_ti
                                                         float max_norm, ga_clip* __restrict__ clip) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     double acc0 = 0.0, acc1 = 0.0;
-    for (int64_t tile = (int64_t)blockIdx.x * kWavesPer + wave; tile < n_tiles;
-         tile += (int64_t)gridDim.x * kWavesPer) {
-        const TileRec rec = a.tiles[tile];
+    for (int64_t slot = (int64_t)blockIdx.x * kWavesPer + wave; slot < n_tiles;
+         slot += (int64_t)gridDim.x * kWavesPer) {
+        const TileRec rec = a.tiles[slot];
+        const int64_t tile = rec.tile;
         float g[8];
         uint32_t dmask;
         if (rec.flags & kTileWhole) mean_grad_whole<T, LEV>(a, tile, rec, lane, g);

@@ -103,101 +103,98 @@ __device__ __forceinline__ void mean_grad_whole(const GradArgs& a, int64_t tile,
 }
 
 // The same of a tile that straddles a layer boundary or holds the tail (0 past
-// P); bit 4q + e of dmask: the element's layer decays.  Each group resolves its
-// own layer, between those of the tile's first and last element; one whose 4
-// elements lie in one layer is a vector load, the others go element by element.
+// P); bit 4q + e of dmask: the element's layer decays.  Each group of 4 resolves
+// its own layer, between those of the tile's first and last element; one whose
+// elements lie in one layer is a vector load, of the others each element's
+// place is found once, before the workers' loop.
 template <int T, int LEV>
 __device__ __forceinline__ void mean_grad_part(const GradArgs& a, int64_t tile, const TileRec& rec, int lane,
                                                float (&g)[8], uint32_t& dmask) {
     constexpr int SZ = kSize<T>;
     constexpr int V = kInFlight<LEV>;
-    TreeAcc<LEV, 8> tree;
-    uint32_t cnt = 0;
-    int64_t i[2], start[2];
-    int32_t layer[2];
-    bool vec[2], part[2];
     dmask = 0;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        i[q] = group_at(tile, lane, q);
+        const int64_t i = group_at(tile, lane, q);
         int32_t lo = (int32_t)rec.layer, hi = lo + (int32_t)(rec.flags >> kTileSpanShift);
-        if (hi > a.L - 1) hi = a.L - 1;
         while (lo < hi) {
             const int32_t mid = (lo + hi) >> 1;
-            if (a.offsets[mid + 1] <= i[q]) lo = mid + 1;
+            if (a.offsets[mid + 1] <= i) lo = mid + 1;
             else hi = mid;
         }
-        layer[q] = lo;
-        start[q] = a.offsets[lo];
-        vec[q] = i[q] + 4 <= a.offsets[lo + 1];
-        part[q] = !vec[q] && i[q] < a.P;
-        if (vec[q]) {
+        const int64_t start = a.offsets[lo];
+        const bool vec = i + 4 <= a.offsets[lo + 1], part = !vec && i < a.P;
+        int32_t layer[4];
+        uint64_t at[4];
+        if (vec) {
             dmask |= a.decay[lo] ? 0xfu << (4 * q) : 0u;
-        } else if (part[q]) {
+        } else if (part) {
             int32_t l = lo;
-            for (int e = 0; e < 4 && i[q] + e < a.P; ++e) {
-                while (a.offsets[l + 1] <= i[q] + e) ++l;
-                dmask |= a.decay[l] ? 1u << (4 * q + e) : 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (i + e < a.P) {
+                    while (a.offsets[l + 1] <= i + e) ++l;
+                    dmask |= a.decay[l] ? 1u << (4 * q + e) : 0u;
+                }
+                // past P: the last element again, set to 0 below
+                const int64_t in = i + e < a.P ? i + e : a.P - 1;
+                layer[e] = l;
+                at[e] = (uint64_t)((in - a.offsets[l]) * SZ);
             }
         }
-    }
-    for (int32_t w0 = 0; w0 < a.W; w0 += V) {
-        float f[V][8];
+        TreeAcc<LEV, 4> tree;
+        uint32_t cnt = 0;
+        for (int32_t w0 = 0; w0 < a.W; w0 += V) {
+            float f[V][4];
 #pragma unroll
-        for (int u = 0; u < V; ++u)
+            for (int u = 0; u < V; ++u)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (vec[q]) {
+                for (int e = 0; e < 4; ++e) f[u][e] = 0.f;
+            // workers past W are read as the last one and not added
+            if (vec) {
                 uint64_t base[V];
                 Raw<T, 4> x[V];
 #pragma unroll
-                for (int u = 0; u < V; ++u)
-                    base[u] = a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + layer[q]];
+                for (int u = 0; u < V; ++u) base[u] = a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + lo];
 #pragma unroll
-                for (int u = 0; u < V; ++u) x[u].load(base[u] + (uint64_t)((i[q] - start[q]) * SZ));
+                for (int u = 0; u < V; ++u) x[u].load(base[u] + (uint64_t)((i - start) * SZ));
+#pragma unroll
+                for (int u = 0; u < V; ++u) x[u].widen(f[u]);
+            } else if (part) {
+                uint64_t base[V][4];
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        base[u][e] = a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + layer[e]];
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[u][e] = load_one<T>(base[u][e] + at[e]);
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[u][e] = i + e < a.P ? f[u][e] : 0.f;
+            }
+            if constexpr (LEV == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[4 * q + e] = f[0][e];
+            } else {
 #pragma unroll
                 for (int u = 0; u < V; ++u) {
-                    float h[4];
-                    x[u].widen(h);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f[u][4 * q + e] = h[e];
-                }
-            } else if (part[q]) {
-                int32_t l = layer[q];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (i[q] + e < a.P) {
-                        while (a.offsets[l + 1] <= i[q] + e) ++l;
-                        const uint64_t at = (uint64_t)((i[q] + e - a.offsets[l]) * SZ);
-#pragma unroll
-                        for (int u = 0; u < V; ++u)
-                            f[u][4 * q + e] =
-                                load_one<T>(a.ptrs[(int64_t)(w0 + u < a.W ? w0 + u : a.W - 1) * a.L + l] + at);
+                    if (w0 + u < a.W) {
+                        tree.push(f[u], cnt);
+                        ++cnt;
                     }
                 }
             }
         }
-        if constexpr (LEV == 1) {
+        if constexpr (LEV > 1) {
+            float s[4];
+            tree.result((uint32_t)a.W, s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = f[0][e];
-            return;
-        } else {
-#pragma unroll
-            for (int u = 0; u < V; ++u) {
-                if (w0 + u < a.W) {
-                    tree.push(f[u], cnt);
-                    ++cnt;
-                }
-            }
+            for (int e = 0; e < 4; ++e) g[4 * q + e] = s[e] * a.inv_w;
         }
-    }
-    if constexpr (LEV > 1) {
-        float s[8];
-        tree.result((uint32_t)a.W, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = s[e] * a.inv_w;
     }
 }
 

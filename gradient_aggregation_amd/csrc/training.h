@@ -12,9 +12,12 @@ namespace ga {
 // A wavefront takes kTile consecutive elements of the fused row.
 constexpr int kTile = 512;
 
-// Where a tile's gradients are: the layer its first element lies in, and that
-// layer's start in the fused row.
+// A tile and where its gradients are: the layer its first element lies in, and
+// that layer's start in the fused row.  The table holds the tiles that are not
+// whole first, the others in order: those few take several times as long and
+// would end last.
 struct TileRec {
+    int64_t tile;       // elements [tile * kTile, (tile + 1) * kTile) of the fused row
     int64_t start;      // first element of the layer
     uint32_t layer;
     uint32_t flags;     // kTileWhole | kTileDecay | layers after this one in the tile << kTileSpanShift

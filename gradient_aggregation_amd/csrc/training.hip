@@ -88,17 +88,23 @@ ga_status ga_adamw_create(int32_t W, int32_t n_layers, const int64_t* layer_nume
         offs[l + 1] = offs[l] + layer_numel[l];
         flags[l] = decay ? decay[l] != 0 : 1;
     }
-    int32_t l = 0;
-    for (int64_t t = 0; t < o->n_tiles; ++t) {
-        const int64_t e0 = t * ga::kTile;
-        while (offs[l + 1] <= e0) ++l;
-        tiles[t].start = offs[l];
-        tiles[t].layer = (uint32_t)l;
-        const int64_t last = (e0 + ga::kTile < info.P ? e0 + ga::kTile : info.P) - 1;
-        int32_t end = l;
-        while (offs[end + 1] <= last) ++end;
-        tiles[t].flags = (offs[l + 1] >= e0 + ga::kTile ? ga::kTileWhole : 0u) | (flags[l] ? ga::kTileDecay : 0u) |
-                         ((uint32_t)(end - l) << ga::kTileSpanShift);
+    ga::TileRec* next = tiles;
+    for (const bool whole : {false, true}) {
+        int32_t l = 0;
+        for (int64_t t = 0; t < o->n_tiles; ++t) {
+            const int64_t e0 = t * ga::kTile;
+            while (offs[l + 1] <= e0) ++l;
+            if ((offs[l + 1] >= e0 + ga::kTile) != whole) continue;
+            const int64_t last = (e0 + ga::kTile < info.P ? e0 + ga::kTile : info.P) - 1;
+            int32_t end = l;
+            while (offs[end + 1] <= last) ++end;
+            next->tile = t;
+            next->start = offs[l];
+            next->layer = (uint32_t)l;
+            next->flags = (whole ? ga::kTileWhole : 0u) | (flags[l] ? ga::kTileDecay : 0u) |
+                          ((uint32_t)(end - l) << ga::kTileSpanShift);
+            ++next;
+        }
     }
     char* d = nullptr;
     hipError_t e = hipGetDevice(&o->device);
