@@ -570,9 +570,10 @@ ga_status ga_grad_norm(const ga_adamw* opt, const uint64_t* d_layer_ptrs, float 
  * ga_grad_norm, times d_clip->scale where d_clip is given:
  *   m <- beta1 m + (1 - beta1) g          v <- beta2 v + (1 - beta2) g^2
  *   w <- w (1 - lr * weight_decay) - lr/(1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
- * (weight_decay taken as 0 on the layers without decay), in binary32; the new
- * w is also rounded into d_copy.  Where d_clip->skip is set, nothing is
- * written.  8-bit states: a block's new moments are scaled by 448 over their
+ * (weight_decay taken as 0 on the layers without decay, an eps between 0 and
+ * 2^-126 as 2^-126), in binary32; the new w is also rounded into d_copy.
+ * Where d_clip->skip is set, nothing is written.
+ * 8-bit states: a block's new moments are scaled by 448 over their
  * largest magnitude (at least 2^-100); m is rounded to nearest even; v's root
  * is raised to 2^-6 of the scaled range where it is not zero (so that it never
  * rounds to zero under a gradient) and rounded up or down at random, with bits
