@@ -60,7 +60,8 @@ _lib = None
 class AdamWParams(ctypes.Structure):
     """ga_adamw_params."""
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
-                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("t", ctypes.c_int64)]
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("m_rounding", ctypes.c_int32),
+                ("t", ctypes.c_int64)]
 
 
 class AdamWStatePtrs(ctypes.Structure):

@@ -14,9 +14,13 @@
 // Codes are e4m3: 4 exponent bits, 3 mantissa bits.  The block maximum is a
 // reduction over the lanes that hold the block's 256 elements, in registers;
 // the second moment is held as its square root, which halves its range in
-// powers of two, and is rounded at random: with beta2 = 0.999 a steady second
-// moment moves by 0.05% per step, a code's step is 6% to 12%, and rounding to
-// nearest would never leave the code it is at.
+// powers of two.  Both are rounded at random: a code's step is 6% to 12%, and a
+// moment that moves by less than half of that per step would never leave the
+// code it is at if it were rounded to nearest.  A second moment with beta2 =
+// 0.999 moves by 0.1% of its distance; a first moment by (1 - beta1) of its:
+// after a gradient that becomes zero, weights would go on moving for ever
+// (2800 steps at beta1 = 0.99: 12901 times lr, where the recurrence itself gives
+// 114).  m to nearest stays as a choice, for states that were kept that way.
 #include "grads.h"
 
 namespace ga {
@@ -33,6 +37,23 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     x = (x ^ (x >> 16)) * 0xB7E15163u;
     x = (x ^ (x >> 15)) * 0x6A09E667u;
     return x ^ (x >> 16);
+}
+
+// Counters of m's bits are this far from those of v's: the two are rounded
+// independently.
+constexpr uint32_t kSeedM = 0xBB67AE85u;
+
+// x cut at random to the grid of the codes: `bits` (below 2^20, a fraction of a
+// step) is added to the 20 mantissa bits that go.  Below 2^-6 the codes are
+// evenly spaced, like the binary32 values with 3 mantissa bits from 2^-6 to
+// 2^-5: such an x is lifted there and lowered again, both exact but for what
+// is below 2^-20 of a step.  0 stays 0, NaN stays NaN.
+__device__ __forceinline__ float cut_at_random(float x, uint32_t bits) {
+    float a = fabsf(x);
+    a = a > kCodeMax ? kCodeMax : a;
+    const float lift = a < 0x1p-6f ? 0x1p-6f : 0.f;
+    const uint32_t z = (__float_as_uint(a + lift) + bits) & 0xfff00000u;
+    return copysignf(__uint_as_float(z) - lift, x);
 }
 
 // 4 consecutive binary32 values at element i of p, 0 past P.
@@ -237,8 +258,17 @@ __device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a
             cv = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (rnd[0] & 0xffff0000u) | 0x8000u, cv, 1);
             cv = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (rnd[1] << 16) | 0x8000u, cv, 2);
             cv = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], (rnd[1] & 0xffff0000u) | 0x8000u, cv, 3);
-            int cm = __builtin_amdgcn_cvt_pk_fp8_f32(mn[4 * q] * mu, mn[4 * q + 1] * mu, 0, false);
-            cm = __builtin_amdgcn_cvt_pk_fp8_f32(mn[4 * q + 2] * mu, mn[4 * q + 3] * mu, cm, true);
+            float z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = mn[4 * q + e] * mu;
+            if (a.m_rounding == GA_ROUND_RANDOM) {
+                const uint32_t mr[2] = {mix(pair + kSeedM), mix(pair + kSeedM + 1u)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[e] = cut_at_random(z[e], (e & 1 ? mr[e / 2] >> 12 & 0xffff0u : (mr[e / 2] & 0xffffu) << 4) | 8u);
+            }
+            int cm = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
+            cm = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], cm, true);
             if (WHOLE || q * GA_STATE_BLOCK < P) {
                 *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + e0 + at[q]) = (uint32_t)cm;
                 *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + e0 + at[q]) = (uint32_t)cv;

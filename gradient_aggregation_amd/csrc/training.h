@@ -44,6 +44,7 @@ struct Adamw {
 struct StepArgs {
     float lr_t, beta1, beta2, c1, c2, eps, rbc2, keep;   // see k_adamw
     uint32_t seed;
+    int32_t m_rounding;   // of 8-bit codes: a ga_rounding
     float* w;
     void* m;
     void* v;

@@ -162,6 +162,8 @@ ga_status ga_adamw_step(const ga_adamw* opt, const uint64_t* d_layer_ptrs, const
     if (!finite_at_least(params->lr, 0.f) || !finite_at_least(params->eps, 0.f) ||
         !finite_at_least(params->weight_decay, 0.f))
         return invalid("lr, eps and weight_decay must be finite and not negative");
+    if (o->bits == 8 && params->m_rounding != GA_ROUND_RANDOM && params->m_rounding != GA_ROUND_NEAREST)
+        return invalid("unknown m_rounding");
     if (d_copy && copy_dtype != GA_FP16 && copy_dtype != GA_BF16) return invalid("the copy is GA_FP16 or GA_BF16");
     if (!aligned(d_layer_ptrs, 8) || !aligned(d_w, 16) || !aligned(state->m, 16) || !aligned(state->v, 16) ||
         (d_copy && !aligned(d_copy, 16)) || (d_clip && !aligned(d_clip, 16)) ||
@@ -182,6 +184,7 @@ ga_status ga_adamw_step(const ga_adamw* opt, const uint64_t* d_layer_ptrs, const
     a.rbc2 = (float)(1.0 / sqrt(1.0 - pow(b2, (double)params->t)));
     a.keep = (float)(1.0 - lr * (double)params->weight_decay);
     a.seed = (uint32_t)((uint64_t)params->t * 0x9E3779B9u + 0x7F4A7C15u);
+    a.m_rounding = params->m_rounding;
     a.w = d_w;
     a.m = state->m;
     a.v = state->v;

@@ -8,6 +8,7 @@ current stream, allocate nothing and do not synchronize.
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import Optional, Sequence
 
 import torch
@@ -19,6 +20,7 @@ MAX_GROUPS = 1024
 MAX_DIM = 1 << 20
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: GA_BF16}
 CODES = torch.float8_e4m3fn
+ROUNDINGS = {"random": 0, "nearest": 1}
 
 
 def _dtype(t, what: str) -> int:
@@ -42,10 +44,22 @@ class Clip:
 class AdamWState:
     """Moments of the P parameters.  32 bits: m, v float32 [P].  8 bits: m, v
     float8_e4m3fn [n_blocks][256] codes with float32 scales [n_blocks]; v holds
-    the square root of the second moment (see gradagg.h)."""
+    the square root of the second moment (see gradagg.h).
 
-    def __init__(self, m, v, m_scale=None, v_scale=None):
-        self.m, self.v, self.m_scale, self.v_scale = m, v, m_scale, v_scale
+    m_rounding (8 bits): how the steps round m's codes, "random" as in the state
+    of empty_state(), or "nearest", under which a moment that moves by less than
+    half a code's step per step stays where it is.  A state made without saying
+    which is rounded to nearest, as such states always were, and warns."""
+
+    def __init__(self, m, v, m_scale=None, v_scale=None, m_rounding: Optional[str] = None):
+        if m_rounding is None:
+            m_rounding = "nearest"
+            if m_scale is not None:
+                warnings.warn("8-bit first moments rounded to nearest do not follow slow changes of the gradient: "
+                              "say m_rounding=\"random\" (or \"nearest\", to repeat earlier results)", stacklevel=2)
+        if m_rounding not in ROUNDINGS:
+            raise ValueError("m_rounding must be \"random\" or \"nearest\", got %r" % (m_rounding,))
+        self.m, self.v, self.m_scale, self.v_scale, self.m_rounding = m, v, m_scale, v_scale, m_rounding
 
 
 class AdamW:
@@ -95,7 +109,8 @@ class AdamW:
             return AdamWState(*(torch.zeros(self.P, dtype=torch.float32, device=device) for _ in range(2)))
         codes = [torch.zeros((self.n_blocks, STATE_BLOCK), dtype=torch.uint8, device=device).view(CODES)
                  for _ in range(2)]
-        return AdamWState(*codes, *(torch.zeros(self.n_blocks, dtype=torch.float32, device=device) for _ in range(2)))
+        scales = [torch.zeros(self.n_blocks, dtype=torch.float32, device=device) for _ in range(2)]
+        return AdamWState(*codes, *scales, m_rounding="random")
 
     def grad_norm(self, layer_ptrs, clip: Clip, max_norm: float = float("inf"), grad=None) -> None:
         """Norm of the workers' mean gradient into `clip`; the mean gradient
@@ -122,7 +137,7 @@ class AdamW:
             cdt = _dtype(copy.dtype, "copy")
         _check(lib().ga_adamw_step(
             self._h, _dev(layer_ptrs, torch.int64, self.W * len(self.layer_numels), "layer_ptrs"),
-            AdamWParams(lr, beta1, beta2, eps, weight_decay, t), _dev(w, torch.float32, self.P, "w"), ptrs,
+            AdamWParams(lr, beta1, beta2, eps, weight_decay, ROUNDINGS[state.m_rounding], t), _dev(w, torch.float32, self.P, "w"), ptrs,
             None if clip is None else _dev(clip.record, torch.float32, 4, "clip"),
             None if copy is None else _dev(copy, copy.dtype, self.P, "copy"), cdt, _stream_ptr()))
 

@@ -494,13 +494,26 @@ ga_status ga_bucket_reduce_layers(const ga_buckets* buckets, int32_t b, const ui
 /* Consecutive elements of the fused vector that share a scale in 8-bit states. */
 #define GA_STATE_BLOCK 256
 
-/* AdamW hyper-parameters.  t: the step, counted from 1. */
+/*
+ * How the first moment's 8-bit codes are rounded.  At random, a moment that
+ * moves by less than a code's step per step still moves on average.  To
+ * nearest, it stays at its code wherever a step would move it by less than half
+ * of the code's step (6% to 12% of the value): it then neither follows a
+ * gradient that changes slowly against beta1 nor decays under one that has become
+ * zero, and its weight goes on moving.  Only for runs that have to repeat
+ * results made that way.
+ */
+typedef enum { GA_ROUND_RANDOM = 0, GA_ROUND_NEAREST = 1 } ga_rounding;
+
+/* AdamW hyper-parameters.  t: the step, counted from 1.  m_rounding: a
+   ga_rounding, read with 8-bit states only. */
 typedef struct {
     float lr;
     float beta1;
     float beta2;
     float eps;
     float weight_decay;
+    int32_t m_rounding;
     int64_t t;
 } ga_adamw_params;
 
@@ -574,16 +587,18 @@ ga_status ga_grad_norm(const ga_adamw* opt, const uint64_t* d_layer_ptrs, float 
  * 2^-126 as 2^-126), in binary32; the new w is also rounded into d_copy.
  * Where d_clip->skip is set, nothing is written.
  * 8-bit states: a block's new moments are scaled by 448 over their
- * largest magnitude (at least 2^-100); m is rounded to nearest even; v's root
- * is raised to 2^-6 of the scaled range where it is not zero (so that it never
- * rounds to zero under a gradient) and rounded up or down at random, with bits
- * that are a fixed function of the element's index and t, so that a second
- * moment that moves by less than a code's step per step still moves on average.
+ * largest magnitude (at least 2^-100); v's root is raised to 2^-6 of the scaled
+ * range where it is not zero (so that it never rounds to zero under a gradient).
+ * Both are rounded to one of the two neighbouring codes at random (m: as
+ * params->m_rounding says), with bits that are a fixed function of the element's
+ * index and t, others for m than for v: a value a fraction f of a step above the
+ * lower code's magnitude becomes the upper one when f + (r + 1/2)/2^16 >= 1, r one
+ * of 2^16 equally likely numbers.  A zero stays zero.
  *   d_w: [P] binary32 in/out.  d_copy: [P] of copy_dtype (GA_FP16 or
  *   GA_BF16), or NULL.  d_clip: NULL or a record of ga_grad_norm.
  * Errors: GA_ERR_INVALID (NULL argument, a missing scale, t < 1, beta1 or
- * beta2 outside [0, 1), lr, eps or weight_decay negative or not finite, a
- * copy of another type), GA_ERR_ALIGN (d_w, m, v, d_copy and d_clip 16 bytes,
+ * beta2 outside [0, 1), lr, eps or weight_decay negative or not finite, an
+ * unknown m_rounding with 8-bit states, a copy of another type), GA_ERR_ALIGN (d_w, m, v, d_copy and d_clip 16 bytes,
  * scales 4 bytes), GA_ERR_DEVICE.
  */
 ga_status ga_adamw_step(const ga_adamw* opt, const uint64_t* d_layer_ptrs, const ga_adamw_params* params,
