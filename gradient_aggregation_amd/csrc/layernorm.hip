@@ -3,8 +3,12 @@
 //
 // Forward: a row is read once and stays in registers, spread over T threads as
 // V vectors of 16 bytes each; its mean and then the sum of squared deviations
-// from that mean are reduced across the threads, so a row far from zero loses
-// nothing.  Backward: one pass over the rows as well; each thread keeps the
+// from that mean are reduced across the threads.  A mean of n values is off by
+// several roundings of their size, which matters where that is many times the
+// row's deviation: there the deviations are summed as well, and their mean
+// corrects the first one (constant binary32 rows near 10000, 1001 wide, came out
+// up to 0.68 from their bias).  Such rows take 6% to 15% longer (16384 x 4096,
+// 4096 x 12288 bf16), those past 16384 elements 21%; the others do not.  Backward: one pass over the rows as well; each thread keeps the
 // weight and the two weight-gradient sums of its columns in registers over all
 // the rows its workgroup takes, and the workgroup writes them as one partial row
 // at the end.  The partial rows of each group are added in a fixed order.
@@ -157,10 +161,24 @@ __device__ __forceinline__ float team_sum(float x, float* buf) {
     return t;
 }
 
+// Whether a row's mean, as it was first rounded, has to be corrected: past four
+// deviations.  Up to there the error that it leaves in y is at most four times
+// that of a row about zero.  The same for all threads of a team, whose sums have
+// the same bits; false where the row holds an infinity or NaN.
+__device__ __forceinline__ bool far_from_zero(float mean, float var, float eps) {
+    return mean * mean > 16.f * (var + eps);
+}
+
+// The correction: off is the deviations' mean, var their mean square.
+__device__ __forceinline__ void correct(float& mean, float& var, float off) {
+    mean += off;
+    var = var > off * off ? var - off * off : 0.f;
+}
+
 template <int X, int P, int T, int V>
 __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim) {
     constexpr int N = kVec<X>, R = kTeamRows<T>;
-    __shared__ float red[2][kTeamWaves<T>];
+    __shared__ float red[3][kTeamWaves<T>];
     const int t = threadIdx.x % T;
     float gamma[V][N], beta[V][N];
     int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / T;
@@ -208,7 +226,7 @@ __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim
         }
         const int64_t next = row + (int64_t)gridDim.x * R;
         if (next < a.rows) load_row(next);
-        const float mean = team_sum<T>(sum, red[0]) * inv_dim;
+        float mean = team_sum<T>(sum, red[0]) * inv_dim;
         // only now has the whole team read the row, which the sum may overwrite
         if (a.sum) {
 #pragma unroll
@@ -231,12 +249,24 @@ __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim
                     if (e < left) sq = fmaf(f[v][e], f[v][e], sq);
             }
         }
-        const float var = team_sum<T>(sq, red[1]) * inv_dim;
+        float var = team_sum<T>(sq, red[1]) * inv_dim, off = 0.f;
+        if (far_from_zero(mean, var, a.eps)) {
+            float sd = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int left = dim - (v * T + t) * N;
+#pragma unroll
+                for (int e = 0; e < N; ++e) sd += e < left ? f[v][e] : 0.f;
+            }
+            off = team_sum<T>(sd, red[2]) * inv_dim;
+            correct(mean, var, off);
+        }
         const float rstd = 1.f / sqrtf(var + a.eps);
+        const float shift = -off * rstd;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) f[v][e] = fmaf(f[v][e] * rstd, gamma[v][e], beta[v][e]);
+            for (int e = 0; e < N; ++e) f[v][e] = fmaf(fmaf(f[v][e], rstd, shift), gamma[v][e], beta[v][e]);
             store_part<X, true>(f[v], reinterpret_cast<uint64_t>(a.y) + (uint64_t)(row * a.ldy), (v * T + t) * N, dim);
         }
         if (t == 0) {
@@ -250,7 +280,7 @@ __global__ __launch_bounds__(kTeamThreads<T>) void k_ln_fwd(LnFwd a, int32_t dim
 template <int X, int P>
 __global__ __launch_bounds__(kLongThreads) void k_ln_fwd_long(LnFwd a, int64_t dim) {
     constexpr int N = kVec<X>, T = kLongThreads;
-    __shared__ float red[2][T / 64];
+    __shared__ float red[3][T / 64];
     const float inv_dim = (float)(1.0 / (double)dim);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const uint64_t xr = reinterpret_cast<uint64_t>(a.x) + (uint64_t)(row * a.ldx);
@@ -288,24 +318,36 @@ __global__ __launch_bounds__(kLongThreads) void k_ln_fwd_long(LnFwd a, int64_t d
 #pragma unroll
             for (int e = 0; e < N; ++e) sum += f[e];
         }
-        const float mean = team_sum<T>(sum, red[0]) * inv_dim;
+        const float first = team_sum<T>(sum, red[0]) * inv_dim;
         float sq = 0.f;
         for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
             float f[N];
             again(c, f);
 #pragma unroll
             for (int e = 0; e < N; ++e)
-                if (c + e < dim) sq = fmaf(f[e] - mean, f[e] - mean, sq);
+                if (c + e < dim) sq = fmaf(f[e] - first, f[e] - first, sq);
         }
-        const float var = team_sum<T>(sq, red[1]) * inv_dim;
+        float mean = first, var = team_sum<T>(sq, red[1]) * inv_dim, off = 0.f;
+        if (far_from_zero(mean, var, a.eps)) {
+            float sd = 0.f;
+            for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
+                float f[N];
+                again(c, f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) sd += c + e < dim ? f[e] - first : 0.f;
+            }
+            off = team_sum<T>(sd, red[2]) * inv_dim;
+            correct(mean, var, off);
+        }
         const float rstd = 1.f / sqrtf(var + a.eps);
+        const float shift = -off * rstd;
         for (int64_t c = (int64_t)threadIdx.x * N; c < dim; c += T * N) {
             float f[N], gamma[N], beta[N];
             again(c, f);
             load_param<P>(gamma, a.gamma, c, dim, 1.f);
             load_param<P>(beta, a.beta, c, dim, 0.f);
 #pragma unroll
-            for (int e = 0; e < N; ++e) f[e] = fmaf((f[e] - mean) * rstd, gamma[e], beta[e]);
+            for (int e = 0; e < N; ++e) f[e] = fmaf(fmaf(f[e] - first, rstd, shift), gamma[e], beta[e]);
             store_part<X>(f, yr, c, dim);
         }
         if (threadIdx.x == 0) {

@@ -637,7 +637,10 @@ typedef struct {
 /*
  * Forward over `rows` rows (0: nothing is launched):
  *   s = x, or fl(x + residual) rounded to x_dtype when residual->data is given
- *   mean = sum(s)/dim, rstd = 1/sqrt(sum((s - mean)^2)/dim + eps)   (binary32)
+ *   mean = sum(s)/dim, rstd = 1/sqrt(sum((s - mean)^2)/dim + eps)   (binary32;
+ *          where |mean| is more than 4/rstd, the mean of the deviations from it
+ *          corrects the mean: a row far from zero, constant or nearly so, loses
+ *          nothing)
  *   y = (s - mean) * rstd * gamma + beta, rounded once to x_dtype
  * residual and sum: NULL, or rows of x_dtype; sum receives s.  gamma, beta:
  * [dim] of p_dtype, or NULL for 1 and 0.  d_mean, d_rstd: [rows] binary32, or
