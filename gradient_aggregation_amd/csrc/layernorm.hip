@@ -521,8 +521,10 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_bwd(LnBwd a, int32_t dim, in
         }
     }
     if (!done) return;
-    // few partial rows: the group's workgroup that ends last adds them, in their order
+    // few partial rows: the group's workgroup that ends last adds them, in their order.  Each wavefront waits for its
+    // own stores: the barrier does not, and the release, thread 0's, writes back to memory what the cache holds then.
     __shared__ uint32_t last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0)
         last = __hip_atomic_fetch_add(done + group, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
