@@ -192,7 +192,7 @@ __device__ __forceinline__ void adamw_tile(const GradArgs& ga, const StepArgs& a
         for (int e = 0; e < 4; ++e) {
             const int k = 4 * q + e;
             // the hardware reciprocal is within 1 ulp of 1/x for the denominators there are: eps is 0 or
-            // normal, and the root of the least v is 2^-74.5
+            // normal, the root of the least v is 2^-74.5, and the largest are below 2^126
             const float up = mn[k] * __builtin_amdgcn_rcpf(fmaf(root[k], a.rbc2, a.eps));
             const float kp = WHOLE ? keep : (dmask >> k) & 1u ? a.keep : 1.f;
             w[q][e] = fmaf(-a.lr_t, up, w[q][e] * kp);

@@ -182,6 +182,12 @@ ga_status ga_adamw_step(const ga_adamw* opt, const uint64_t* d_layer_ptrs, const
     // a denormal eps would have no reciprocal in the kernel's hardware instruction
     a.eps = params->eps > 0.f && params->eps < 0x1p-126f ? 0x1p-126f : params->eps;
     a.rbc2 = (float)(1.0 / sqrt(1.0 - pow(b2, (double)params->t)));
+    // nor has the hardware's reciprocal a denormal result: the quotient's denominator and lr's factor are scaled alike
+    if (a.eps >= 0x1p125f) {
+        a.eps *= 0x1p-4f;
+        a.rbc2 *= 0x1p-4f;
+        a.lr_t *= 0x1p-4f;
+    }
     a.keep = (float)(1.0 - lr * (double)params->weight_decay);
     a.seed = (uint32_t)((uint64_t)params->t * 0x9E3779B9u + 0x7F4A7C15u);
     a.m_rounding = params->m_rounding;

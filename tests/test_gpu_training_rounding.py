@@ -1,5 +1,6 @@
 """8-bit first moments rounded at random, on the GPU: the codes of one step
-against their definition, and many steps against the exact recurrence."""
+against their definition, and many steps against the exact recurrence.  The
+update at the largest eps."""
 import math
 
 import pytest
@@ -103,3 +104,18 @@ def test_turned_gradients(ga, factor, noise, beta1, beta2):
     steady = [float(((b[0] - a[0]) * turn.base.double().sign())[::2].mean()) for a, b in (got, want)]
     assert abs(steady[0] - steady[1]) <= (turn.steps - turn.BEFORE) / 8 + turn.bound(beta1, want)
     assert math.isfinite(float(w.abs().sum()))
+
+
+@pytest.mark.parametrize("eps", [8e37, 9e37, 3e38])
+def test_an_eps_whose_reciprocal_is_denormal(ga, eps):
+    """m / (root + eps) where 1/eps is below the normal range."""
+    n = 700
+    g, w = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    m = (torch.linspace(-1, 1, n) * 3e38).cuda()
+    opt = ga.AdamW([n])
+    table = torch.tensor([g.data_ptr()], dtype=torch.int64, device="cuda")
+    want = 1 - 0.25 * m.double() / f32(eps)                  # beta1 = 1/2 at t = 1: half of m over one half
+    opt.step(table, w, ga.AdamWState(m, torch.ones(n, device="cuda")), t=1, lr=0.25, beta1=0.5, beta2=0.5, eps=eps)
+    # lr's factor, a reciprocal of 2 units, three products and the difference
+    off = float((w.double() - want).abs().max())
+    assert off <= 8 * U * (1 + 0.25 * 3e38 / 8e37)
