@@ -207,10 +207,15 @@ def _torch():
 
 
 def _stream_ptr() -> int:
-    """The current stream of the current device (without the stream object that
-    torch.cuda.current_stream() makes: 0.2 against 2.6 us)."""
-    C = _torch()._C
-    return C._cuda_getCurrentRawStream(C._cuda_getDevice())
+    """The current stream of the current device: without the stream object that
+    torch.cuda.current_stream() makes (0.2 against 2.6 us) where torch has the
+    calls that return its address, which are not public."""
+    torch = _torch()
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if device is None or stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream(device())
 
 
 def _dev(t, dtype, min_numel: int, name: str):
