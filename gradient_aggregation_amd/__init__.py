@@ -144,6 +144,8 @@ def lib() -> ctypes.CDLL:
         L.ga_bucket_reduce_layers.restype = st
         L.ga_bucket_reduce_layers.argtypes = [_VP, ctypes.c_int32, _VP, _VP, _VP, ctypes.POINTER(SGD), _VP, _VP,
                                               ctypes.c_int32, _VP]
+        L.ga_training_version.restype = ctypes.c_int32
+        L.ga_training_version.argtypes = []
         i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
         rows = ctypes.POINTER(Rows)
         L.ga_adamw_create.restype = st

@@ -53,6 +53,8 @@ ga_status check_rows(const ga_rows* r, int64_t rows, int64_t dim, int64_t size, 
 
 extern "C" {
 
+int32_t ga_training_version(void) { return GA_TRAINING_VERSION; }
+
 ga_status ga_adamw_create(int32_t W, int32_t n_layers, const int64_t* layer_numel, ga_dtype grad_dtype,
                           int32_t state_bits, const uint8_t* decay, ga_adamw** out) {
     if (!out) return invalid("out is NULL");

@@ -70,6 +70,10 @@ extern "C" {
 #endif
 
 #define GA_ABI_VERSION 4
+/* Version of the training-step operators (ga_adamw, ga_grad_norm, ga_layernorm,
+   GA_BF16) alone.  1, which had neither this number nor ga_training_version: the
+   first; 2: ga_adamw_params has m_rounding. */
+#define GA_TRAINING_VERSION 2
 #define GA_MAX_WORKERS 1024
 #define GA_MAX_CHUNKS 65536
 /* Most elements per worker (P) of a plan or an SGD call: every 1-D grid of
@@ -111,8 +115,11 @@ typedef struct {
 
 typedef struct ga_plan ga_plan;
 
-/* Version of this interface (GA_ABI_VERSION). */
+/* Version of this interface without the training-step operators (GA_ABI_VERSION). */
 int32_t ga_abi_version(void);
+/* Version of the training-step operators (GA_TRAINING_VERSION).  A library
+   without this symbol has their first version, or none of them. */
+int32_t ga_training_version(void);
 
 /* Static name of a status code. */
 const char* ga_status_str(ga_status s);
