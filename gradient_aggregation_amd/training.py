@@ -4,6 +4,13 @@ Argument marshalling only, like the rest of the binding: the operators are the
 HIP kernels behind ga_grad_norm, ga_adamw_step, ga_layernorm_forward and
 ga_layernorm_backward, specified in include/gradagg.h.  Calls run on the
 current stream, allocate nothing and do not synchronize.
+
+A handle owns one workspace.  AdamW.grad_norm and LayerNorm.backward use it: two
+such calls on one handle must not run at the same time.  Give each stream that
+runs them a handle of its own, or order the streams with events.  Calls that did
+overlap can leave the handle's count of ended workgroups wrong, and later calls
+on it without a result: make a new handle then.  The other calls may overlap.
+A captured call uses its handle's memory at every replay: keep the handle.
 """
 from __future__ import annotations
 
@@ -115,7 +122,8 @@ class AdamW:
     def grad_norm(self, layer_ptrs, clip: Clip, max_norm: float = float("inf"), grad=None) -> None:
         """Norm of the workers' mean gradient into `clip`; the mean gradient
         itself into `grad` ([P] float32) where given.  layer_ptrs: int64 tensor
-        of the W*L gradient tensors' addresses, worker-major."""
+        of the W*L gradient tensors' addresses, worker-major.  Not at the same
+        time as another grad_norm on this handle (on another stream)."""
         _check(lib().ga_grad_norm(self._h, _dev(layer_ptrs, torch.int64, self.W * len(self.layer_numels), "layer_ptrs"),
                                   max_norm, _dev(grad, torch.float32, self.P, "grad"),
                                   _dev(clip.record, torch.float32, 4, "clip"), _stream_ptr()))
@@ -216,7 +224,8 @@ class LayerNorm:
     def backward(self, dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dsum=None, groups: int = 1) -> None:
         """dx of the forward pass at x (its sum_out where it had a residual),
         plus dsum where given; dgamma, dbeta: [groups][dim] in any of the three
-        types, each group its own run of consecutive rows."""
+        types, each group its own run of consecutive rows.  Not at the same time
+        as another backward on this handle (on another stream)."""
         n = self._count(x)
         pdt = torch.float32 if dgamma is None else dgamma.dtype
         _check(lib().ga_layernorm_backward(

@@ -563,7 +563,8 @@ typedef struct ga_adamw ga_adamw;
  * calls below allocate nothing, do not synchronize and may be captured into a
  * graph (the parameters are then those of the capture).  Steps on one handle
  * may run at the same time; two ga_grad_norm calls may not (issue them on one
- * stream or order them with events).
+ * stream or order them with events): two that overlap can leave the handle's
+ * count of ended workgroups wrong, and calls after them without a result.
  */
 ga_status ga_adamw_create(int32_t W, int32_t n_layers, const int64_t* layer_numel, ga_dtype grad_dtype,
                           int32_t state_bits, const uint8_t* decay, ga_adamw** out);
@@ -670,7 +671,8 @@ ga_status ga_layernorm_forward(const ga_layernorm* ln, int64_t rows, const ga_ro
  * Row sums and the weight gradients' sums are binary32, each in a fixed order.
  * With rows = 0, zeros are written to them.  dx may be dy, dsum or x itself.
  * Uses the handle's workspace: not concurrently with another backward pass on
- * the same handle (issue them on one stream or order them with events).
+ * the same handle (issue them on one stream or order them with events; as for
+ * ga_grad_norm, an overlap can spoil the calls after it too).
  * Errors as ga_layernorm_forward, and GA_ERR_INVALID when groups < 1 or does
  * not divide rows, or only one of d_dgamma and d_dbeta is given;
  * GA_ERR_UNSUPPORTED for groups > GA_MAX_GROUPS.
