@@ -106,6 +106,23 @@ def test_turned_gradients(ga, factor, noise, beta1, beta2):
     assert math.isfinite(float(w.abs().sum()))
 
 
+@pytest.mark.parametrize("factor", [0.7, 0.5])
+def test_second_moments_of_changed_gradients(ga, factor):
+    """Second moments that move by far less than a code's step per step, while
+    the largest of their block stays."""
+    n = 4096
+    turn = model.Turn(n, factor, device="cuda")
+    want = model.exact(turn, n, turn.steps, 0.9, 0.999, device="cuda")[-1]
+    opt = ga.AdamW([n], state_bits=8)
+    g, w, state = torch.empty(n, device="cuda"), torch.zeros(n, device="cuda"), opt.empty_state()
+    table = torch.tensor([g.data_ptr()], dtype=torch.int64, device="cuda")
+    for t in range(1, turn.steps + 1):
+        g.copy_(turn(t))
+        opt.step(table, w, state, t=t, lr=0.0, beta1=0.9, beta2=0.999)
+    v = (state.v.double() * state.v_scale.double()[:, None]).square().reshape(-1)
+    assert abs(turn.second((w, v), want) - 1) <= turn.second_bound()
+
+
 @pytest.mark.parametrize("eps", [8e37, 9e37, 3e38])
 def test_an_eps_whose_reciprocal_is_denormal(ga, eps):
     """m / (root + eps) where 1/eps is below the normal range."""

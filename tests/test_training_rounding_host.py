@@ -59,3 +59,15 @@ def test_model_of_turned_gradients(factor, noise, beta1, beta2):
     bound = turn.bound(beta1, want)
     assert abs(turn.moved(model.run(*args, watch=(turn.BEFORE,))) - turn.moved(want)) <= bound
     assert abs(turn.moved(model.run(*args, m_how="nearest", watch=(turn.BEFORE,))) - turn.moved(want)) > bound
+
+
+@pytest.mark.parametrize("factor", [0.7, 0.5])
+def test_model_of_second_moments(factor):
+    """Second moments that move by far less than a code's step per step, while
+    the largest of their block stays: rounded at random they follow, to nearest
+    and down they do not."""
+    turn = model.Turn(2048, factor)
+    args = (turn, 2048, turn.steps, 0.9, 0.999)
+    want = model.exact(*args)[-1]
+    off = {how: abs(turn.second(model.run(*args, v_how=how)[-1], want) - 1) for how in ("random", "nearest", "down")}
+    assert off["random"] <= turn.second_bound() < min(off["nearest"], off["down"]), off
