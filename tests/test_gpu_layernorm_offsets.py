@@ -84,6 +84,16 @@ def test_little_spread(ga, dim, offset):
         check(ga, x, res=(0.5 * x).contiguous())
 
 
+@pytest.mark.parametrize("dim,rows", [(61, 70000), (509, 19000), (2047, 4800), (4093, 4800), (8189, 2400), (12289, 1200),
+                                      (16390, 2400)])
+def test_far_and_near_rows_in_turn(ga, dim, rows):
+    """A workgroup's rows, two or three of them, need the correction or not."""
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    x = torch.randn(rows, dim, generator=gen, device="cuda")
+    far = torch.rand(rows, 1, generator=gen, device="cuda") < 0.5
+    check(ga, x + torch.where(far, 1e4, 0.0))
+
+
 def test_one_far_element(ga):
     """An outlier at the row's start or end."""
     for at in (0, -1):
