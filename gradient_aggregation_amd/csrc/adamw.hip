@@ -8,8 +8,8 @@
 // (gradients) + 8 (w) + 16 (binary32 moments) or 4 + 1/16 (codes and scales) +
 // 2 (low-precision copy) bytes, against some 40 to 70 instructions.  61M
 // parameters of 16 binary16 workers: 565 us (6.0 TB/s); 61M with 8-bit states,
-// bf16 gradients and copy: 162 us (6.1 TB/s); 7.6M with binary32 states, bf16
-// gradients and copy: 38 us (5.6 TB/s); 29,354: 6 us.
+// bf16 gradients and copy: 164 us (6.0 TB/s); 7.6M with binary32 states, bf16
+// gradients and copy: 37 us (5.7 TB/s); 29,354: 6 us.
 //
 // Codes are e4m3: 4 exponent bits, 3 mantissa bits.  The block maximum is a
 // reduction over the lanes that hold the block's 256 elements, in registers;

@@ -8,14 +8,18 @@
 // row's deviation: there the deviations are summed as well, and their mean
 // corrects the first one (constant binary32 rows near 10000, 1001 wide, came out
 // up to 0.68 from their bias).  Such rows take 6% to 15% longer (16384 x 4096,
-// 4096 x 12288 bf16), those past 16384 elements 21%; the others do not.  Backward: one pass over the rows as well; each thread keeps the
-// weight and the two weight-gradient sums of its columns in registers over all
-// the rows its workgroup takes, and the workgroup writes them as one partial row
-// at the end.  The partial rows of each group are added in a fixed order.
+// 4096 x 12288 bf16), those past 16384 elements 21%; the others do not.
+//
+// Backward: one pass over the rows as well; each thread keeps the weight and the
+// two weight-gradient sums of its columns in registers over all the rows its
+// workgroup takes, and the workgroup writes them as one partial row at the end.
+// The partial rows of each group are added in a fixed order.
 //
 // Bound by memory: b * (2 to 4) bytes per element forward, b * (3 to 4)
-// backward, against some 15 to 25 instructions.  16384 x 4096 bf16 rows: 94 us
-// forward with the residual (5.7 TB/s), 92 us backward with it (5.8 TB/s).
+// backward, against some 15 to 25 instructions.  16384 x 4096 bf16 rows, one
+// pass after the other: 93 to 99 us forward with the residual (5.8 to 5.4 TB/s: it
+// differs between cards, not between runs on one), 95 us backward with it (5.6
+// TB/s).
 // The backward pass takes one workgroup of 1024 threads per CU: with two of 512
 // as many rows are on their way, but twice the partial rows are written and
 // read (105 us), with two of 256 the chip waits for memory (110 us).
@@ -670,7 +674,7 @@ __global__ __launch_bounds__(256) void k_ln_params_end(const float* __restrict__
 
 // Calls f<T, V> with the team that holds a row of dim elements.  Forward: 16
 // elements per thread of a workgroup of 256 where that is enough (16384 x 4096
-// bf16 rows with a residual: 94 us; 98 with 8 per thread of 512), and no more
+// bf16 rows with a residual, on one card: 94 us; 98 with 8 per thread of 512), and no more
 // threads than a narrow row needs (60000 x 64 rows: 10 us with 16 threads, 27
 // with 64).
 #define GA_TEAM(T, V) \

@@ -602,6 +602,8 @@ ga_status ga_grad_norm(const ga_adamw* opt, const uint64_t* d_layer_ptrs, float 
  * index and t, others for m than for v: a value a fraction f of a step above the
  * lower code's magnitude becomes the upper one when f + (r + 1/2)/2^16 >= 1, r one
  * of 2^16 equally likely numbers.  A zero stays zero.
+ * A gradient that is not finite spoils the moments of its whole block, whose
+ * scales it makes so: clip by a record of ga_grad_norm, whose skip keeps it out.
  *   d_w: [P] binary32 in/out.  d_copy: [P] of copy_dtype (GA_FP16 or
  *   GA_BF16), or NULL.  d_clip: NULL or a record of ga_grad_norm.
  * Errors: GA_ERR_INVALID (NULL argument, a missing scale, t < 1, beta1 or

@@ -106,6 +106,33 @@ def test_turned_gradients(ga, factor, noise, beta1, beta2):
     assert math.isfinite(float(w.abs().sum()))
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("rounding", ["random", "nearest"])
+def test_a_gradient_that_is_not_finite_stays_in_its_block(ga, bad, rounding):
+    """It spoils the block's moments, and of the weights its own at once."""
+    n = 1024
+    gen = torch.Generator().manual_seed(5)
+    values = torch.randn(3, n, generator=gen)
+    runs = []
+    for x in (0.0, bad):
+        g = values.clone().cuda()
+        g[1, 300] = x
+        opt = ga.AdamW([n], state_bits=8)
+        w, state = torch.zeros(n, device="cuda"), opt.empty_state()
+        state.m_rounding = rounding
+        for t in (1, 2):
+            table = torch.tensor([g[t - 1].data_ptr()], dtype=torch.int64, device="cuda")
+            opt.step(table, w, state, t=t, lr=0.1)
+        runs.append((w, state))
+    (w0, s0), (w1, s1) = runs
+    others = torch.ones(n, dtype=torch.bool, device="cuda")
+    others[300] = False
+    assert torch.equal(w0[others], w1[others]) and not math.isfinite(float(w1[300]))
+    for k in ("m", "v"):
+        a, b = ((getattr(s, k).float() * getattr(s, k + "_scale")[:, None]) for s in (s0, s1))
+        assert torch.equal(a[[0, 2, 3]], b[[0, 2, 3]]) and not bool(torch.isfinite(b[1]).any())
+
+
 @pytest.mark.parametrize("factor", [0.7, 0.5])
 def test_second_moments_of_changed_gradients(ga, factor):
     """Second moments that move by far less than a code's step per step, while
