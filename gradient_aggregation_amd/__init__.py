@@ -57,11 +57,18 @@ _VP = ctypes.c_void_p
 _lib = None
 
 
-class AdamWParams(ctypes.Structure):
-    """ga_adamw_params."""
+class AdamWParamsLayout(ctypes.Structure):
+    """ga_adamw_params, its fields in the order of memory."""
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("m_rounding", ctypes.c_int32),
                 ("t", ctypes.c_int64)]
+
+
+class AdamWParams(AdamWParamsLayout):
+    """ga_adamw_params.  m_rounding, which lies before t, comes last here."""
+
+    def __init__(self, lr=0.0, beta1=0.0, beta2=0.0, eps=0.0, weight_decay=0.0, t=0, m_rounding=0):
+        super().__init__(lr, beta1, beta2, eps, weight_decay, m_rounding, t)
 
 
 class AdamWStatePtrs(ctypes.Structure):
@@ -155,8 +162,8 @@ def lib() -> ctypes.CDLL:
         L.ga_grad_norm.restype = st
         L.ga_grad_norm.argtypes = [_VP, _VP, f32, _VP, _VP, _VP]
         L.ga_adamw_step.restype = st
-        L.ga_adamw_step.argtypes = [_VP, _VP, ctypes.POINTER(AdamWParams), _VP, ctypes.POINTER(AdamWStatePtrs), _VP, _VP, st,
-                                    _VP]
+        L.ga_adamw_step.argtypes = [_VP, _VP, ctypes.POINTER(AdamWParamsLayout), _VP,
+                                    ctypes.POINTER(AdamWStatePtrs), _VP, _VP, st, _VP]
         L.ga_layernorm_create.restype = st
         L.ga_layernorm_create.argtypes = [i64, st, st, i32, ctypes.POINTER(_VP)]
         L.ga_layernorm_destroy.restype = None

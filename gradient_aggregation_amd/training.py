@@ -20,7 +20,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import _VP, GA_BF16, AdamWParams, AdamWStatePtrs, Rows, _check, _dev, _stream_ptr, lib
+from . import _VP, GA_BF16, AdamWParamsLayout, AdamWStatePtrs, Rows, _check, _dev, _stream_ptr, lib
 
 STATE_BLOCK = 256
 MAX_GROUPS = 1024
@@ -57,6 +57,8 @@ class AdamWState:
     of empty_state(), or "nearest", under which a moment that moves by less than
     half a code's step per step stays where it is.  A state made without saying
     which is rounded to nearest, as such states always were, and warns."""
+
+    m_rounding = "nearest"      # of a state pickled before there was a choice
 
     def __init__(self, m, v, m_scale=None, v_scale=None, m_rounding: Optional[str] = None):
         if m_rounding is None:
@@ -145,7 +147,8 @@ class AdamW:
             cdt = _dtype(copy.dtype, "copy")
         _check(lib().ga_adamw_step(
             self._h, _dev(layer_ptrs, torch.int64, self.W * len(self.layer_numels), "layer_ptrs"),
-            AdamWParams(lr, beta1, beta2, eps, weight_decay, ROUNDINGS[state.m_rounding], t), _dev(w, torch.float32, self.P, "w"), ptrs,
+            AdamWParamsLayout(lr, beta1, beta2, eps, weight_decay, ROUNDINGS[state.m_rounding], t),
+            _dev(w, torch.float32, self.P, "w"), ptrs,
             None if clip is None else _dev(clip.record, torch.float32, 4, "clip"),
             None if copy is None else _dev(copy, copy.dtype, self.P, "copy"), cdt, _stream_ptr()))
 

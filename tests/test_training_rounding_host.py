@@ -34,6 +34,15 @@ def test_states_say_how_they_are_rounded(ga):
         ga.AdamWState(one, one, one, one, m_rounding="up")
 
 
+def test_what_was_made_before_there_was_a_choice(ga):
+    """Parameters in their earlier order, and states without the attribute (a
+    pickled one, say)."""
+    p = ga.AdamWParams(1e-3, 0.9, 0.999, 1e-8, 0.1, 5)
+    assert (p.t, p.m_rounding) == (5, 0) and p.weight_decay == pytest.approx(0.1)
+    assert ga.AdamWParams(lr=1.0, t=3).t == 3 and ga.AdamWParams(t=3, m_rounding=1).m_rounding == 1
+    assert ga.AdamWState.__new__(ga.AdamWState).m_rounding == "nearest"
+
+
 def test_step_refuses_an_unknown_rounding(ga):
     block = (ctypes.c_int32 * 256)()
     handle, step = ctypes.addressof(block), ga.lib().ga_adamw_step
