@@ -220,11 +220,10 @@ def _stream_ptr() -> int:
     torch.cuda.current_stream() makes (0.2 against 2.6 us) where torch has the
     calls that return its address, which are not public."""
     torch = _torch()
-    device = getattr(torch._C, "_cuda_getDevice", None)
-    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if device is None or stream is None:
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
         return torch.cuda.current_stream().cuda_stream
-    return stream(device())
 
 
 def _dev(t, dtype, min_numel: int, name: str):
