@@ -81,6 +81,21 @@ class Rows(ctypes.Structure):
     _fields_ = [("data", _VP), ("ld", ctypes.c_int64)]
 
 
+class Images(ctypes.Structure):
+    """ga_images: a channels-last tensor, its position and sample strides in elements."""
+    _fields_ = [("data", _VP), ("ld", ctypes.c_int64), ("sample", ctypes.c_int64)]
+
+
+class RoutingPtrs(ctypes.Structure):
+    """ga_routing."""
+    _fields_ = [("experts", _VP), ("gates", _VP), ("lse", _VP)]
+
+
+class LoadPtrs(ctypes.Structure):
+    """ga_load."""
+    _fields_ = [("counts", _VP), ("probs", _VP), ("tokens", _VP), ("loss", _VP), ("slope", _VP)]
+
+
 def lib() -> ctypes.CDLL:
     """The loaded library.  Raises if it has not been built."""
     global _lib
@@ -172,6 +187,28 @@ def lib() -> ctypes.CDLL:
         L.ga_layernorm_forward.argtypes = [_VP, i64, rows, rows, _VP, _VP, f32, rows, rows, _VP, _VP, _VP]
         L.ga_layernorm_backward.restype = st
         L.ga_layernorm_backward.argtypes = [_VP, i64, rows, rows, _VP, _VP, _VP, rows, rows, i32, _VP, _VP, st, _VP]
+        images = ctypes.POINTER(Images)
+        L.ga_layers_version.restype = i32
+        L.ga_layers_version.argtypes = []
+        L.ga_groupnorm_create.restype = st
+        L.ga_groupnorm_create.argtypes = [i32, i32, st, st, st, i32, ctypes.POINTER(_VP)]
+        L.ga_groupnorm_destroy.restype = None
+        L.ga_groupnorm_destroy.argtypes = [_VP]
+        L.ga_groupnorm_forward.restype = st
+        L.ga_groupnorm_forward.argtypes = [_VP, i64, i64, images, _VP, _VP, f32, images, _VP, _VP, _VP]
+        L.ga_groupnorm_backward.restype = st
+        L.ga_groupnorm_backward.argtypes = [_VP, i64, i64, images, images, _VP, _VP, _VP, _VP, images, i32, _VP, _VP,
+                                            st, _VP]
+        L.ga_router_create.restype = st
+        L.ga_router_create.argtypes = [i32, i32, st, i32, i32, st, ctypes.POINTER(_VP)]
+        L.ga_router_destroy.restype = None
+        L.ga_router_destroy.argtypes = [_VP]
+        L.ga_router_forward.restype = st
+        L.ga_router_forward.argtypes = [_VP, i64, rows, _VP, i32, ctypes.POINTER(RoutingPtrs),
+                                        ctypes.POINTER(LoadPtrs), _VP]
+        L.ga_router_backward.restype = st
+        L.ga_router_backward.argtypes = [_VP, i64, rows, _VP, ctypes.POINTER(RoutingPtrs), _VP, _VP, f32, f32, rows,
+                                         _VP]
         _lib = L
     return _lib
 
@@ -616,11 +653,15 @@ def sgd_momentum_apply(grad, w, v, lr: float, mu: float) -> None:
 
 
 _TRAINING = ("AdamW", "AdamWState", "Clip", "LayerNorm")
+_LAYERS = ("GroupNorm", "Router", "RouterLoad", "Routing")
 
 
 def __getattr__(name: str):
-    # the training-step operators need torch, which the plan arithmetic above does not
+    # the training-step and layer operators need torch, which the plan arithmetic above does not
     if name in _TRAINING:
         from . import training
         return getattr(training, name)
+    if name in _LAYERS:
+        from . import layers
+        return getattr(layers, name)
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -74,6 +74,8 @@ extern "C" {
    GA_BF16) alone.  1, which had neither this number nor ga_training_version: the
    first; 2: ga_adamw_params has m_rounding. */
 #define GA_TRAINING_VERSION 2
+/* Version of the layer operators (ga_groupnorm, ga_router) alone. */
+#define GA_LAYERS_VERSION 1
 #define GA_MAX_WORKERS 1024
 #define GA_MAX_CHUNKS 65536
 /* Most elements per worker (P) of a plan or an SGD call: every 1-D grid of
@@ -120,6 +122,9 @@ int32_t ga_abi_version(void);
 /* Version of the training-step operators (GA_TRAINING_VERSION).  A library
    without this symbol has their first version, or none of them. */
 int32_t ga_training_version(void);
+/* Version of the layer operators (GA_LAYERS_VERSION).  A library without this
+   symbol has none of them. */
+int32_t ga_layers_version(void);
 
 /* Static name of a status code. */
 const char* ga_status_str(ga_status s);
@@ -683,6 +688,187 @@ ga_status ga_layernorm_backward(const ga_layernorm* ln, int64_t rows, const ga_r
                                 const void* d_gamma, const float* d_mean, const float* d_rstd, const ga_rows* dsum,
                                 const ga_rows* dx, int32_t groups, void* d_dgamma, void* d_dbeta, ga_dtype dp_dtype,
                                 hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer operators: group norm with an activation over images, and the router
+ * of a mixture of experts with its per-expert counts and balance loss.  As in
+ * layer norm, the weight gradients, or the counts, come per worker.
+ * ---------------------------------------------------------------------- */
+
+/* Most channels of a group norm. */
+#define GA_MAX_CHANNELS 65536
+
+/* none: z.  relu: z where z > 0, else 0.  silu: z / (1 + exp(-z)). */
+typedef enum { GA_ACT_NONE = 0, GA_ACT_RELU = 1, GA_ACT_SILU = 2 } ga_activation;
+
+/* Images, channels last: channel c of position s of sample n is at data +
+   n * sample + s * ld + c elements.  Positions and samples must not overlap (with
+   more than one: ld >= channels, sample >= channels, and either a sample's
+   positions end before the next sample or the samples are interleaved).  Aligned
+   to its element. */
+typedef struct {
+    const void* data;
+    int64_t ld;
+    int64_t sample;
+} ga_images;
+
+typedef struct ga_groupnorm ga_groupnorm;
+
+/*
+ * Group norm over images of `channels` channels of x_dtype in `groups` groups of
+ * consecutive channels, with weight and bias vectors of p_dtype (GA_FP32 or
+ * x_dtype), followed by an activation, on the current device.  The handle owns
+ * a workspace that both passes use; backward == 0 leaves out the part that only
+ * the backward pass needs (then ga_groupnorm_backward refuses the handle).
+ * GA_ERR_INVALID: channels < 1, groups < 1 or no divisor of channels, a type or an
+ * activation that is not listed; GA_ERR_UNSUPPORTED: channels > GA_MAX_CHANNELS.
+ */
+ga_status ga_groupnorm_create(int32_t channels, int32_t groups, ga_dtype x_dtype, ga_dtype p_dtype,
+                              ga_activation activation, int32_t backward, ga_groupnorm** out);
+
+/* Destroy a handle (NULL is ignored).  No call using it may still be queued. */
+void ga_groupnorm_destroy(ga_groupnorm* gn);
+
+/*
+ * Forward over `samples` samples of `positions` positions (either 0: nothing is
+ * launched).  For each sample and group, over its positions and channels:
+ *   mean = sum(x)/n, rstd = 1/sqrt(sum((x - mean)^2)/n + eps)      (binary32, the
+ *          sums about a value of the data itself: a group far from zero, constant
+ *          or nearly so, loses nothing; deviations past 1.8e19 have squares past
+ *          binary32, and rstd is 0 or NaN)
+ *   y = activation((x - mean) * rstd * gamma + beta), rounded once to x_dtype
+ * gamma, beta: [channels] of p_dtype, or NULL for 1 and 0.  d_mean, d_rstd:
+ * [samples][groups] binary32, or NULL.  y may be x itself.
+ * Uses the handle's workspace: not concurrently with another call on the same
+ * handle (issue them on one stream or order them with events; calls that overlap
+ * give wrong results).
+ * Errors: GA_ERR_INVALID: NULL x or y, a negative size, images that overlap, eps
+ * not positive and finite; GA_ERR_ALIGN: a tensor not aligned to its element;
+ * GA_ERR_UNSUPPORTED: samples * groups or positions past 2^31 - 1.
+ */
+ga_status ga_groupnorm_forward(const ga_groupnorm* gn, int64_t samples, int64_t positions, const ga_images* x,
+                               const void* d_gamma, const void* d_beta, float eps, const ga_images* y, float* d_mean,
+                               float* d_rstd, hipStream_t stream);
+
+/*
+ * Backward over the same images.  With xh = (x - mean) * rstd, z = xh * gamma +
+ * beta, dz = dy * activation'(z) (relu: 0 where z <= 0) and h = dz * gamma:
+ *   dx = rstd * (h - mean_group(h) - xh * mean_group(h * xh))
+ *   dgamma[w] = sum of dz * xh,  dbeta[w] = sum of dz   over the samples of worker w
+ * The samples form `workers` runs of samples/workers consecutive ones, each with
+ * its own weight gradients: d_dgamma, d_dbeta: [workers][channels] of dp_dtype
+ * (any ga_dtype), or both NULL.  All sums are binary32, each in a fixed order.  With
+ * no samples or positions, zeros are written to them.  dx may be dy or x itself.
+ * Uses the handle's workspace, as the forward pass.
+ * Errors as ga_groupnorm_forward, and GA_ERR_INVALID when workers < 1 or does not
+ * divide samples, or only one of d_dgamma and d_dbeta is given;
+ * GA_ERR_UNSUPPORTED for workers > GA_MAX_WORKERS.
+ */
+ga_status ga_groupnorm_backward(const ga_groupnorm* gn, int64_t samples, int64_t positions, const ga_images* dy,
+                                const ga_images* x, const void* d_gamma, const void* d_beta, const float* d_mean,
+                                const float* d_rstd, const ga_images* dx, int32_t workers, void* d_dgamma,
+                                void* d_dbeta, ga_dtype dp_dtype, hipStream_t stream);
+
+#define GA_MAX_EXPERTS 1024
+/* Most experts of a token. */
+#define GA_MAX_TOPK 32
+
+/* Over what a balance loss takes its counts and means: all workers' tokens, or
+   each worker's own (the losses of the workers are then averaged). */
+typedef enum { GA_BALANCE_ALL = 0, GA_BALANCE_WORKER = 1 } ga_balance;
+
+typedef struct ga_router ga_router;
+
+/*
+ * Router of E = `experts` experts, k of them to a token, for the tokens of
+ * `workers` workers, on the current device.  x_dtype: the logits' type (any
+ * ga_dtype).  normalize: the gates of a token sum to 1.  The handle owns the
+ * workspace of the counts.
+ * GA_ERR_INVALID: experts < 1, k outside [1, experts], workers < 1, an unknown type
+ * or balance; GA_ERR_UNSUPPORTED: experts > GA_MAX_EXPERTS, k > GA_MAX_TOPK,
+ * workers > GA_MAX_WORKERS.
+ */
+ga_status ga_router_create(int32_t experts, int32_t k, ga_dtype x_dtype, int32_t workers, int32_t normalize,
+                           ga_balance balance, ga_router** out);
+
+/* Destroy a handle (NULL is ignored).  No call using it may still be queued. */
+void ga_router_destroy(ga_router* router);
+
+/* A token's experts and their gates, [tokens][k], and the logarithm of the sum of
+   its logits' exponentials, [tokens]. */
+typedef struct {
+    int32_t* experts;
+    float* gates;
+    float* lse;
+} ga_routing;
+
+/*
+ * The workers' use of the experts.  S is 1 (GA_BALANCE_ALL) or the number of
+ * workers.
+ *   counts [workers][E]: times that a token of the worker took the expert
+ *   probs  [workers][E]: sum of the expert's probability over the worker's tokens
+ *   tokens [workers]:    tokens that are present
+ *   loss   [2]:          the balance loss and the z loss
+ *   slope  [S][E + 1]:   for the backward pass: the derivative of the balance loss
+ *                        to a token's probability of each expert; then that of the
+ *                        z loss to a token's lse, divided by the lse
+ */
+typedef struct {
+    int32_t* counts;
+    float* probs;
+    int32_t* tokens;
+    float* loss;
+    float* slope;
+} ga_load;
+
+/*
+ * Route `tokens` tokens: runs of tokens/workers consecutive ones for each worker.
+ * With l a token's logits and p = exp(l - lse), lse = log(sum(exp(l))):
+ *   select != 0: experts <- the k largest logits in descending order, among equal
+ *     ones the lowest index first.  A logit of -infinity is never selected, nor
+ *     is a NaN: where fewer than k are left, the remaining experts are -1.
+ *   select == 0: experts is read (a selection made elsewhere; one outside [0, E)
+ *     is no expert, the same one twice counts twice).
+ *   gates <- p at the experts; with `normalize`, divided by their sum (formed from
+ *     the logits, so that it does not underflow); 0 at no expert.
+ * A token is absent where d_mask ([tokens] bytes, or NULL) is 0, or where all its
+ * logits are -infinity: its gates and lse are 0, its experts, if selected, are -1, and it
+ * counts nowhere, whatever its logits are.
+ * With load (NULL: not formed), and F, P, n its counts, probs and tokens (of all
+ * workers together, or of each worker, whose losses are then averaged):
+ *   balance = E / (k n^2) * sum_e F_e P_e (1 where both are uniform)
+ *   z = sum(lse^2) / n          (no tokens: both 0)
+ * A NaN or +infinity makes its token's gates and lse, and the losses, NaN; the
+ * squares of an lse past 1.8e19 are infinite.  Sums
+ * are in binary32 over a workgroup's tokens, in binary64 beyond, in a fixed order.
+ *   logits: rows of E.  routing->gates and ->lse may be NULL; with load, all of
+ *   its pointers are needed.
+ * With load, it uses the handle's workspace: not concurrently with another such
+ * call on the same handle (issue them on one stream or order them with events; an
+ * overlap can spoil the calls after it too).
+ * Errors: GA_ERR_INVALID: a NULL argument, tokens < 0 or not a multiple of
+ * workers, rows that overlap; GA_ERR_ALIGN: a buffer not aligned to its
+ * element; GA_ERR_UNSUPPORTED: tokens * k past 2^31 - 1.
+ */
+ga_status ga_router_forward(const ga_router* router, int64_t tokens, const ga_rows* logits, const uint8_t* d_mask,
+                            int32_t select, const ga_routing* routing, const ga_load* load, hipStream_t stream);
+
+/*
+ * Gradient of
+ *   balance * (balance loss) + z * (z loss) + sum of dgates * gates
+ * to the logits, the experts and counts held constant, rounded once to x_dtype.
+ * routing and d_slope are those of the forward pass over the same logits and
+ * mask; p is formed from its lse, and so off by 2^-24 of lse's size.  d_dgates: [tokens][k] binary32, or NULL for 0.  d_slope: NULL only where
+ * balance and z are 0.  dlogits may be logits itself.  Absent tokens: 0.
+ * routing->gates is read with `normalize` and d_dgates only.  A worker's mean gradient
+ * is `workers` times the gradient of the mean over all: scale balance and z so
+ * where the workers' gradients are averaged.
+ * Uses no workspace.  Errors as ga_router_forward, and GA_ERR_INVALID for a
+ * coefficient that is not finite.
+ */
+ga_status ga_router_backward(const ga_router* router, int64_t tokens, const ga_rows* logits, const uint8_t* d_mask,
+                             const ga_routing* routing, const float* d_slope, const float* d_dgates, float balance,
+                             float z, const ga_rows* dlogits, hipStream_t stream);
 
 #ifdef __cplusplus
 }
