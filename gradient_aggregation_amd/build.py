@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgradagg.so")
 SOURCES = ["abi.hip", "buckets.hip", "dense.hip", "variants.hip", "norm.hip", "topk.hip", "gather.hip", "history.hip", "noalloc.hip", "pack.hip",
-           "training.hip", "adamw.hip", "gradnorm.hip", "layernorm.hip", "layers.hip", "groupnorm.hip", "router.hip"]
+           "training.hip", "adamw.hip", "gradnorm.hip", "layernorm.hip", "layers.hip", "groupnorm_fwd.hip", "groupnorm_bwd.hip", "router.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -32,115 +32,18 @@
 // 87 us, 89 with it).
 #include <type_traits>
 
-#include "elements.h"
+#include "rowvec.h"
 #include "training.h"
 
 namespace ga {
 
 namespace {
 
-template <int X>
-constexpr int kVec = 16 / kSize<X>;     // elements of a 128-bit vector
-
 // Rows wider than this do not stay in registers: they are read again in each
 // pass (from the caches, at these lengths).
 constexpr int64_t kInRegisters = 16384;
 constexpr int kLongThreads = 1024;
 constexpr int kBwdThreads = 1024;
-
-// Elements [c, c + N) of a row that ends at dim; those past it are 0.
-template <int X, int N, bool NT = false>
-__device__ __forceinline__ void load_part(Raw<X, N>& r, uint64_t row, int64_t c, int64_t dim) {
-    const uint64_t at = row + (uint64_t)c * kSize<X>;
-    if (c + N <= dim) {
-        r.template load<NT>(at);
-        return;
-    }
-    float f[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = 0.f;
-    if (c < dim) {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (c + e < dim) f[e] = load_one<X>(at + e * kSize<X>);
-    }
-    r.narrow(f);
-}
-
-// The same in two steps, for rows read ahead: the load itself, in which the
-// vector that would pass the end is read from where it ends there instead (a
-// load per element would have to be waited for at once), and the shift that
-// moves its elements into place and fills up with zeros.
-template <int X, int N, bool NT>
-__device__ __forceinline__ void load_ahead(Raw<X, N>& r, uint64_t row, int32_t c, int32_t dim) {
-    if (dim < N) {
-        load_part(r, row, c, dim);
-    } else if (c < dim) {
-        r.template load<NT>(row + (uint64_t)((c < dim - N ? c : dim - N) * kSize<X>));
-    } else {
-#pragma unroll
-        for (int j = 0; j < Raw<X, N>::WORDS; ++j) r.w[j] = 0u;
-    }
-}
-
-template <int X, int N>
-__device__ __forceinline__ void into_place(Raw<X, N>& r, int32_t c, int32_t dim) {
-    static_assert(Raw<X, N>::WORDS == 4, "a 128-bit vector");
-    if (dim < N || dim % N == 0) return;
-    const int past = c + N - dim;
-    const uint32_t s = past > 0 && past < N ? past : 0;   // elements to drop
-    const uint32_t words = s * kSize<X> / 4;
-    if (words & 2u) {
-        r.w[0] = r.w[2];
-        r.w[1] = r.w[3];
-        r.w[2] = r.w[3] = 0u;
-    }
-    if (words & 1u) {
-        r.w[0] = r.w[1];
-        r.w[1] = r.w[2];
-        r.w[2] = r.w[3];
-        r.w[3] = 0u;
-    }
-    if (kSize<X> == 2 && (s & 1u)) {
-        r.w[0] = __builtin_amdgcn_alignbit(r.w[1], r.w[0], 16);
-        r.w[1] = __builtin_amdgcn_alignbit(r.w[2], r.w[1], 16);
-        r.w[2] = __builtin_amdgcn_alignbit(r.w[3], r.w[2], 16);
-        r.w[3] >>= 16;
-    }
-}
-
-template <int X, bool NT = false, int N>
-__device__ __forceinline__ void store_part(const float (&f)[N], uint64_t row, int64_t c, int64_t dim) {
-    const uint64_t at = row + (uint64_t)c * kSize<X>;
-    if (c + N <= dim) {
-        Raw<X, N> r;
-        r.narrow(f);
-        r.template store<NT>(at);
-    } else if (c < dim) {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (c + e < dim) store_one<X>(at + e * kSize<X>, f[e]);
-    }
-}
-
-// N elements of a weight vector from column c (fill where it is not given or
-// past dim).
-template <int P, int N>
-__device__ __forceinline__ void load_param(float (&f)[N], const void* p, int64_t c, int64_t dim, float fill) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = fill;
-    if (!p || c >= dim) return;
-    const uint64_t at = reinterpret_cast<uint64_t>(p) + (uint64_t)c * kSize<P>;
-    if (c + N <= dim) {
-        Raw<P, N> r;
-        r.load(at);
-        r.widen(f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (c + e < dim) f[e] = load_one<P>(at + e * kSize<P>);
-    }
-}
 
 // T threads take a row.  Teams of up to a wavefront share a workgroup of 256;
 // a larger team is a workgroup.
@@ -359,14 +262,6 @@ __global__ __launch_bounds__(kLongThreads) void k_ln_fwd_long(LnFwd a, int64_t d
             if (a.rstd) a.rstd[row] = rstd;
         }
     }
-}
-
-// Where a workgroup's weight-gradient sums go: straight to the result when its
-// group has one part, else to its partial row.
-__device__ __forceinline__ void store_param(void* out, int32_t dtype, int64_t i, float x) {
-    if (dtype == kF32) static_cast<float*>(out)[i] = x;
-    else if (dtype == kF16) store_one<kF16>(reinterpret_cast<uint64_t>(out) + (uint64_t)i * 2, x);
-    else store_one<kB16>(reinterpret_cast<uint64_t>(out) + (uint64_t)i * 2, x);
 }
 
 // Workgroup blockIdx.x = group * parts + part takes rows part * R, (part +
@@ -785,12 +680,17 @@ hipError_t ln_bwd(const LayerNorm& n, const LnBwd& a, hipStream_t s) {
         });
     }
     if (e != hipSuccess || !a.dgamma || parts == 1 || one) return e;
-    hipLaunchKernelGGL(k_ln_params_end, dim3((unsigned)((2 * n.ldp + 63) / 64), (unsigned)a.groups), dim3(256), 0, s,
-                       n.d_parts, n.dim, n.ldp, parts, a.dgamma, a.dbeta, a.dp_dtype);
-    return hipGetLastError();
+    return launch_params_end(n.d_parts, n.dim, n.ldp, parts, a.groups, a.dgamma, a.dbeta, a.dp_dtype, s);
 }
 
 }  // namespace
+
+hipError_t launch_params_end(const float* in, int64_t dim, int64_t ldp, int32_t parts, int32_t groups, void* dgamma,
+                             void* dbeta, int32_t dp_dtype, hipStream_t s) {
+    hipLaunchKernelGGL(k_ln_params_end, dim3((unsigned)((2 * ldp + 63) / 64), (unsigned)groups), dim3(256), 0, s, in, dim,
+                       ldp, parts, dgamma, dbeta, dp_dtype);
+    return hipGetLastError();
+}
 
 hipError_t launch_ln_fwd(const LayerNorm& n, const LnFwd& a, hipStream_t s) {
     if (n.x_dtype == GA_FP32) return ln_fwd<kF32, kF32>(n, a, s);

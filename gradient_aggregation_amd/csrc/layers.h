@@ -14,7 +14,16 @@ struct GroupNorm {
     int32_t x_dtype, p_dtype, act;
     int device;
     int32_t backward;
+    int32_t ldp;           // stride of a partial row (channels rounded up to 4)
+    int32_t rows;          // partial rows of the weight gradients
+    float* d_rows;         // [rows][2][ldp], or nullptr
+    void* d_records;       // kGnRecords of 16 bytes: partial sums of groups
 };
+
+// Partial rows at most, and their bytes.
+constexpr int kGnRows = 512;
+constexpr int64_t kGnRowBytes = (int64_t)16 << 20;
+constexpr int64_t kGnRecords = (int64_t)1 << 20;
 
 struct Images {
     const char* data;

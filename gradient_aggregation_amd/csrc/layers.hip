@@ -98,7 +98,15 @@ ga_status ga_groupnorm_create(int32_t channels, int32_t groups, ga_dtype x_dtype
     n->p_dtype = (int32_t)p_dtype;
     n->act = (int32_t)activation;
     n->backward = backward != 0;
-    const hipError_t e = hipGetDevice(&n->device);
+    n->ldp = (channels + 3) / 4 * 4;
+    const int64_t rows = ga::kGnRowBytes / (2 * (int64_t)sizeof(float) * n->ldp);
+    n->rows = rows < ga::kGnRows ? (int32_t)rows : ga::kGnRows;
+    n->d_rows = nullptr;
+    n->d_records = nullptr;
+    hipError_t e = hipGetDevice(&n->device);
+    if (e == hipSuccess && backward)
+        e = hipMalloc((void**)&n->d_rows, 2 * sizeof(float) * (size_t)n->rows * (size_t)n->ldp);
+    if (e == hipSuccess) e = hipMalloc(&n->d_records, 16 * (size_t)ga::kGnRecords);
     if (e != hipSuccess) {
         const ga_status bad = ga::api_fail(GA_ERR_DEVICE, hipGetErrorString(e));
         (void)hipGetLastError();
@@ -111,7 +119,10 @@ ga_status ga_groupnorm_create(int32_t channels, int32_t groups, ga_dtype x_dtype
 
 void ga_groupnorm_destroy(ga_groupnorm* gn) {
     if (!gn) return;
-    delete reinterpret_cast<ga::GroupNorm*>(gn);
+    ga::GroupNorm* n = reinterpret_cast<ga::GroupNorm*>(gn);
+    if (n->d_rows) (void)hipFree(n->d_rows);
+    if (n->d_records) (void)hipFree(n->d_records);
+    delete n;
 }
 
 ga_status ga_groupnorm_forward(const ga_groupnorm* gn, int64_t samples, int64_t positions, const ga_images* x,

@@ -94,5 +94,9 @@ struct LnBwd {
 
 hipError_t launch_ln_fwd(const LayerNorm& n, const LnFwd& a, hipStream_t s);
 hipError_t launch_ln_bwd(const LayerNorm& n, const LnBwd& a, hipStream_t s);
+// Adds each group's `parts` partial rows of two weight gradients, [groups][parts][2][ldp], in a fixed order; parts = 0
+// writes zeros.
+hipError_t launch_params_end(const float* in, int64_t dim, int64_t ldp, int32_t parts, int32_t groups, void* dgamma,
+                             void* dbeta, int32_t dp_dtype, hipStream_t s);
 
 }  // namespace ga
