@@ -52,8 +52,17 @@ struct Router {
     int32_t E, k, W;
     int32_t x_dtype, normalize, scope;
     int device;
-    double* d_squares;     // [W] sum of lse^2
+    int32_t rows;          // partial loads: kRouterRows, or a row for each worker
+    // one allocation
+    double* d_squares;     // [rows] sums of lse^2
+    double* d_dots;        // [GA_MAX_EXPERTS] parts of the balance loss
+    float* d_probs;        // [rows][E]
+    int32_t* d_counts;     // [rows][E]
+    int32_t* d_tokens;     // [rows]
+    uint32_t* d_done;      // [2] workgroups that have ended; 0 between calls
 };
+
+constexpr int kRouterRows = 512;
 
 struct RouteArgs {
     int64_t T, per_worker;    // tokens, tokens of a worker

@@ -223,7 +223,20 @@ ga_status ga_router_create(int32_t experts, int32_t k, ga_dtype x_dtype, int32_t
     r->scope = (int32_t)balance;
     r->d_squares = nullptr;
     hipError_t e = hipGetDevice(&r->device);
-    if (e == hipSuccess) e = hipMalloc((void**)&r->d_squares, sizeof(double) * (size_t)workers);
+    r->rows = workers > ga::kRouterRows ? workers : ga::kRouterRows;
+    const size_t rows = (size_t)r->rows, all = rows * (size_t)experts;
+    char* d = nullptr;
+    if (e == hipSuccess) e = hipMalloc((void**)&d, 8 * (rows + GA_MAX_EXPERTS) + 4 * (2 * all + rows) + 8);
+    if (e == hipSuccess) {
+        r->d_squares = reinterpret_cast<double*>(d);
+        r->d_dots = r->d_squares + rows;
+        r->d_probs = reinterpret_cast<float*>(r->d_dots + GA_MAX_EXPERTS);
+        r->d_counts = reinterpret_cast<int32_t*>(r->d_probs + all);
+        r->d_tokens = r->d_counts + all;
+        r->d_done = reinterpret_cast<uint32_t*>(r->d_tokens + rows);
+        const uint32_t zeros[2] = {};
+        e = hipMemcpy(r->d_done, zeros, sizeof zeros, hipMemcpyHostToDevice);
+    }
     if (e != hipSuccess) {
         const ga_status bad = ga::api_fail(GA_ERR_DEVICE, hipGetErrorString(e));
         (void)hipGetLastError();

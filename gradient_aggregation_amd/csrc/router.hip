@@ -1,256 +1,659 @@
 // Router of a mixture of experts with its counts and balance loss
-// (ga_router_forward, ga_router_backward): the plainest form.  A wavefront takes a
-// token, up to 16 experts to a lane.
-#include "elements.h"
+// (ga_router_forward, ga_router_backward).
+#include <type_traits>
+
 #include "layers.h"
+#include "rowvec.h"
 
 namespace ga {
 
 namespace {
 
-constexpr int kMost = GA_MAX_EXPERTS / 64;
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr float kLog2e = 1.44269504f;
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
-    return x;
-}
+// ---- teams of L lanes (a power of 2, aligned), all of whose lanes get the result ----
 
-__device__ __forceinline__ int wave_min(int x) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) x = min(x, __shfl_xor(x, off, 64));
-    return x;
-}
-
-// Softmax and selection of one token.
-template <int X>
-__global__ __launch_bounds__(64) void k_route(RouteArgs a, int32_t E, int32_t k, int32_t normalize) {
-    const int lane = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const uint64_t row = reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx);
-        const bool masked = a.mask && !a.mask[t];
-        float l[kMost], top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int e = i * 64 + lane;
-            l[i] = e < E && !masked ? load_one<X>(row + (uint64_t)e * kSize<X>) : -INFINITY;
-            top = fmaxf(top, l[i]);
-        }
-        top = wave_max(top);
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) sum += l[i] == -INFINITY ? 0.f : expf(l[i] - top);
-        sum = lanes_sum_f32<64>(sum);
-        const bool absent = sum == 0.f;
-        const float lse = absent ? 0.f : top + logf(sum);
-        float mine = 0.f, chosen = 0.f;     // lane j: exp(logit - top) of slot j
-        for (int j = 0; j < k; ++j) {
-            int at = -1;
-            if (!a.select) {
-                const int e = a.r.experts[t * k + j];
-                at = e >= 0 && e < E ? e : -1;
-            } else if (!absent) {
-                float best = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kMost; ++i) best = fmaxf(best, l[i]);
-                best = wave_max(best);
-                int first = 1 << 30;
-#pragma unroll
-                for (int i = kMost - 1; i >= 0; --i)
-                    if (l[i] == best) first = i * 64 + lane;
-                first = wave_min(first);
-                if (best > -INFINITY) at = first;
-#pragma unroll
-                for (int i = 0; i < kMost; ++i)
-                    if (i * 64 + lane == at) l[i] = -INFINITY;
-            }
-            float g = 0.f;
-            if (at >= 0 && !absent) {
-                const float x = load_one<X>(row + (uint64_t)at * kSize<X>);
-                g = x == -INFINITY ? 0.f : expf(x - top);
-            }
-            chosen += g;
-            if (lane == j) {
-                mine = g;
-                if (a.select) a.r.experts[t * k + j] = at;
-            }
-        }
-        float by = normalize ? chosen : sum;
-        if (sum != sum) by = sum;
-        if (a.r.gates && lane < k) a.r.gates[t * k + lane] = by == 0.f ? 0.f : mine / by;
-        if (a.r.lse && lane == 0) a.r.lse[t] = lse;
+template <int L, typename OP>
+__device__ __forceinline__ uint32_t team_reduce(uint32_t x, OP op) {
+    if constexpr (L >= 2) x = op(x, lane_move<0xb1>(x));      // xor 1
+    if constexpr (L >= 4) x = op(x, lane_move<0x4e>(x));      // xor 2
+    if constexpr (L >= 8) x = op(x, lane_move<0x141>(x));     // mirror within 8
+    if constexpr (L >= 16) x = op(x, lane_move<0x140>(x));    // mirror within 16
+    if constexpr (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        x = op(r[0], r[1]);
     }
+    if constexpr (L >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        x = op(r[0], r[1]);
+    }
+    return x;
 }
 
-// The load of worker blockIdx.x, from the logits and the experts.
-template <int X>
-__global__ __launch_bounds__(256) void k_load(RouteArgs a, int32_t E, int32_t k, double* __restrict__ out) {
-    __shared__ int count[GA_MAX_EXPERTS];
-    __shared__ float top_of, sum_of;
-    __shared__ double squares;
-    const int64_t w = blockIdx.x;
-    double p[GA_MAX_EXPERTS / 256] = {};
-    int n = 0;
-    for (int e = threadIdx.x; e < GA_MAX_EXPERTS; e += 256) count[e] = 0;
-    if (threadIdx.x == 0) squares = 0.0;
-    for (int64_t t = w * a.per_worker; t < (w + 1) * a.per_worker; ++t) {
-        if (a.mask && !a.mask[t]) continue;
-        const uint64_t row = reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx);
-        __syncthreads();
-        if (threadIdx.x < 64) {
-            float top = -INFINITY, sum = 0.f;
-            for (int e = threadIdx.x; e < E; e += 64) top = fmaxf(top, load_one<X>(row + (uint64_t)e * kSize<X>));
-            top = wave_max(top);
-            for (int e = threadIdx.x; e < E; e += 64) {
-                const float l = load_one<X>(row + (uint64_t)e * kSize<X>);
-                sum += l == -INFINITY ? 0.f : expf(l - top);
-            }
-            sum = lanes_sum_f32<64>(sum);
-            if (threadIdx.x == 0) {
-                top_of = top;
-                sum_of = sum;
-                if (sum != 0.f) {
-                    const double lse = (double)top + log((double)sum);
-                    squares += lse * lse;
-                }
+template <int L>
+__device__ __forceinline__ float team_sum(float x) {
+    return __uint_as_float(team_reduce<L>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+
+template <int L>
+__device__ __forceinline__ float team_max(float x) {
+    return __uint_as_float(team_reduce<L>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+
+// Sum of the lower lanes' values.
+template <int L>
+__device__ __forceinline__ int team_before(int x) {
+    const int ln = threadIdx.x & (L - 1);
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+        const int y = __shfl_up(s, o, L);
+        if (ln >= o) s += y;
+    }
+    return s - x;
+}
+
+// What one lane of a wavefront wrote to LDS, another may now read: the hardware keeps a wavefront's accesses in order,
+// this keeps the compiler's.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A lane's V elements of a row of E: vectors of N elements, those of a team's lanes next to each other.
+template <int X, int L, int V>
+struct Lane {
+    static constexpr int N = kVec<X>, J = V / N;
+    int ln, E;
+
+    __device__ __forceinline__ explicit Lane(int experts) : ln(threadIdx.x & (L - 1)), E(experts) {}
+    __device__ __forceinline__ int column(int i) const { return (i / N * L + ln) * N + i % N; }
+
+    __device__ __forceinline__ void load(Raw<X, N> (&r)[J], uint64_t row) const {
+#pragma unroll
+        for (int j = 0; j < J; ++j) load_ahead<X, N, false>(r[j], row, (j * L + ln) * N, E);
+    }
+
+    // The values; past the row's end, and everywhere of an absent row, -infinity.
+    __device__ __forceinline__ void widen(Raw<X, N> (&r)[J], float (&f)[V], bool present) const {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float t[N];
+            into_place(r[j], (j * L + ln) * N, E);
+            r[j].widen(t);
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[j * N + e] = t[e];
+        }
+        if (E < L * V || !present) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = present && column(i) < E ? f[i] : -INFINITY;
+        }
+    }
+};
+
+// A logit as a number whose order is its own (zeros of both signs alike), below it the index, the lowest on top.
+__device__ __forceinline__ uint64_t key_of(float v, int column) {
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return (uint64_t)(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) << 32 | (uint32_t)~column;
+}
+
+__device__ __forceinline__ float value_of(uint64_t key) {
+    const uint32_t u = (uint32_t)(key >> 32);
+    return __uint_as_float(u ^ ((int32_t)u < 0 ? 0x80000000u : 0xffffffffu));
+}
+
+// Where the partial loads of the workgroups lie: row = worker * parts + part.
+struct LoadParts {
+    float* probs;          // [rows][E]
+    int32_t* counts;       // [rows][E]
+    double* squares;       // [rows]
+    int32_t* tokens;       // [rows]
+    double* dots;          // a part of the balance loss for each chunk of experts
+    uint32_t* done;        // [2]; 0 between calls
+    int32_t parts;
+};
+
+constexpr int kChunk = 16;                                // experts of a chunk
+
+struct LossArgs {
+    ga_load load;
+    int32_t E, k, W, scope;
+};
+
+// Ends the load of chunk `chunk` of the experts: the workers' counts and sums, and the slope; returns the chunk's part
+// of the balance loss in thread 0.  THREADS threads, of which kChunk share an expert's row each.
+struct EndScratch {
+    double p[64][kChunk];
+    int64_t c[64][kChunk];
+    int32_t tokens[GA_MAX_WORKERS];
+    double dot[kChunk];
+};
+
+template <int THREADS>
+__device__ __forceinline__ void sum_tokens(const LossArgs& a, const LoadParts& q, EndScratch& s) {
+    for (int w = threadIdx.x; w < a.W; w += THREADS) s.tokens[w] = 0;
+    __syncthreads();
+    for (int r = threadIdx.x; r < a.W * q.parts; r += THREADS) atomicAdd(&s.tokens[r / q.parts], q.tokens[r]);
+    __syncthreads();
+}
+
+// 1 / tokens, of all workers or of worker w; 0 without tokens.
+__device__ __forceinline__ double share_of(const LossArgs& a, const EndScratch& s, int w) {
+    int64_t n = 0;
+    if (a.scope == GA_BALANCE_ALL) {
+        for (int i = 0; i < a.W; ++i) n += s.tokens[i];
+    } else {
+        n = s.tokens[w];
+    }
+    return n > 0 ? 1.0 / (double)n : 0.0;
+}
+
+template <int THREADS>
+__device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& q, EndScratch& s, int chunk) {
+    constexpr int SLICES = THREADS / kChunk;
+    const int col = threadIdx.x & (kChunk - 1), slice = threadIdx.x / kChunk, e = chunk * kChunk + col;
+    int at_once = 1;                                      // workers taken together
+    while (at_once * 2 <= SLICES && at_once < a.W) at_once *= 2;
+    const int per = SLICES / at_once, wl = slice / per, ps = slice % per;
+    const bool all = a.scope == GA_BALANCE_ALL;
+    const double total = all ? share_of(a, s, 0) : 0.0;
+    double P = 0.0, dot = 0.0;
+    int64_t F = 0;
+    for (int w0 = 0; w0 < a.W; w0 += at_once) {
+        const int w = w0 + wl;
+        double p = 0.0;
+        int64_t c = 0;
+        if (w < a.W && e < a.E) {
+#pragma unroll 4
+            for (int i = ps; i < q.parts; i += per) {
+                const int64_t at = ((int64_t)w * q.parts + i) * a.E + e;
+                p += (double)q.probs[at];
+                c += q.counts[at];
             }
         }
         __syncthreads();
-        if (sum_of == 0.f) continue;
-        ++n;
-        for (int i = 0; i < GA_MAX_EXPERTS / 256; ++i) {
-            const int e = i * 256 + threadIdx.x;
-            if (e < E) {
-                const float l = load_one<X>(row + (uint64_t)e * kSize<X>);
-                p[i] += l == -INFINITY && sum_of == sum_of ? 0.0 : (double)(expf(l - top_of) / sum_of);
-            }
+        s.p[slice][col] = p;
+        s.c[slice][col] = c;
+        __syncthreads();
+        if (ps != 0 || w >= a.W || e >= a.E) continue;
+        for (int i = 1; i < per; ++i) {
+            p += s.p[slice + i][col];
+            c += s.c[slice + i][col];
         }
-        if (threadIdx.x < k) {
-            const int e = a.r.experts[t * k + threadIdx.x];
-            if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+        a.load.probs[(int64_t)w * a.E + e] = (float)p;
+        a.load.counts[(int64_t)w * a.E + e] = (int32_t)c;
+        P += p;
+        F += c;
+        if (!all) {
+            const double share = share_of(a, s, w), slope = (double)c * a.E / a.k * share * share / a.W;
+            a.load.slope[(int64_t)w * (a.E + 1) + e] = (float)slope;
+            dot += slope * p;
         }
     }
     __syncthreads();
-    for (int i = 0; i < GA_MAX_EXPERTS / 256; ++i) {
-        const int e = i * 256 + threadIdx.x;
-        if (e < E) {
-            a.load.counts[w * E + e] = count[e];
-            a.load.probs[w * E + e] = (float)p[i];
+    s.p[slice][col] = all ? P : dot;
+    s.c[slice][col] = F;
+    __syncthreads();
+    if (slice == 0) {
+        for (int i = 1; i < at_once; ++i) {
+            P += s.p[i * per][col];
+            dot += s.p[i * per][col];
+            F += s.c[i * per][col];
         }
+        if (all) {
+            const double slope = (double)F * a.E / a.k * total * total;
+            if (e < a.E) a.load.slope[e] = (float)slope;
+            dot = slope * P;
+        }
+        s.dot[col] = e < a.E ? dot : 0.0;
     }
-    if (threadIdx.x == 0) {
-        a.load.tokens[w] = n;
-        out[w] = squares;
-    }
+    __syncthreads();
+    if (threadIdx.x != 0) return 0.0;
+    double sum = 0.0;
+    for (int i = 0; i < kChunk; ++i) sum += s.dot[i];
+    return sum;
 }
 
-__global__ __launch_bounds__(64) void k_loss(RouteArgs a, int32_t E, int32_t k, int32_t W, int32_t scope,
-                                             const double* __restrict__ squares) {
+// What is not of a chunk: the workers' tokens, the z loss, and the slope's last column.
+template <int THREADS>
+__device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, const EndScratch& s) {
+    const bool all = a.scope == GA_BALANCE_ALL;
+    for (int w = threadIdx.x; w < a.W; w += THREADS) {
+        a.load.tokens[w] = s.tokens[w];
+        if (!all) a.load.slope[(int64_t)w * (a.E + 1) + a.E] = (float)(2.0 * share_of(a, s, w) / a.W);
+    }
+    if (threadIdx.x >= 64) return;
+    const double total = all ? share_of(a, s, 0) : 0.0;
+    double z = 0.0;
+    for (int r = threadIdx.x; r < a.W * q.parts; r += 64) {
+        const double share = all ? total : share_of(a, s, r / q.parts) / a.W;
+        if (share > 0.0) z += q.squares[r] * share;
+    }
+    z = wave_sum_f64(z);
     if (threadIdx.x != 0) return;
-    double loss = 0.0, z = 0.0, all = 0.0;
-    for (int w = 0; w < W; ++w) all += a.load.tokens[w];
-    const int S = scope == GA_BALANCE_ALL ? 1 : W;
-    for (int s = 0; s < S; ++s) {
-        const double n = S == 1 ? all : a.load.tokens[s], share = n > 0 ? 1.0 / n / S : 0.0;
-        for (int e = 0; e < E; ++e) {
-            double F = 0.0, P = 0.0;
-            for (int w = S == 1 ? 0 : s; w < (S == 1 ? W : s + 1); ++w) {
-                F += a.load.counts[(int64_t)w * E + e];
-                P += a.load.probs[(int64_t)w * E + e];
-            }
-            const double slope = n > 0 ? F * E / k / n * share : 0.0;
-            a.load.slope[(int64_t)s * (E + 1) + e] = (float)slope;
-            loss += slope * P;
-        }
-        a.load.slope[(int64_t)s * (E + 1) + E] = (float)(2.0 * share);
-        for (int w = S == 1 ? 0 : s; w < (S == 1 ? W : s + 1); ++w) z += squares[w] * share;
-    }
-    a.load.loss[0] = (float)loss;
     a.load.loss[1] = (float)z;
+    if (all) a.load.slope[a.E] = (float)(2.0 * total);
 }
 
-template <int X>
-__global__ __launch_bounds__(64) void k_route_bwd(RouteArgs a, int32_t E, int32_t k, int32_t normalize, int32_t S,
-                                                  int64_t per_slope) {
-    const int lane = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const uint64_t row = reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx);
-        const uint64_t out = reinterpret_cast<uint64_t>(a.dx) + (uint64_t)(t * a.ldd);
-        float p[kMost], h[kMost], direct[kMost], lse = a.r.lse[t];
-        float any = -INFINITY;
-        const bool masked = a.mask && !a.mask[t];
-        const float* slope = a.slope ? a.slope + t / per_slope * (E + 1) : nullptr;
+// Whether this workgroup is the last of n to get here; what the others stored before is then visible.  Each wavefront
+// waits for its own stores: the barrier does not, and the release, thread 0's, writes back what the cache holds then.
+__device__ __forceinline__ bool last_of(uint32_t* done, uint32_t n) {
+    __shared__ uint32_t last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT) + 1 == n;
+    }
+    __syncthreads();
+    if (!last) return false;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    if (threadIdx.x == 0) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
+constexpr int kEndThreads = 1024;
+
+__global__ __launch_bounds__(kEndThreads) void k_load_end(LossArgs a, LoadParts q) {
+    __shared__ EndScratch s;
+    sum_tokens<kEndThreads>(a, q, s);
+    const double dot = end_chunk<kEndThreads>(a, q, s, (int)blockIdx.x);
+    if (blockIdx.x == 0) end_rest<kEndThreads>(a, q, s);
+    if (threadIdx.x == 0) q.dots[blockIdx.x] = dot;
+    if (!last_of(q.done, gridDim.x) || threadIdx.x != 0) return;
+    double loss = 0.0;
+    for (uint32_t i = 0; i < gridDim.x; ++i) loss += __hip_atomic_load(q.dots + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.load.loss[0] = (float)loss;
+}
+
+// ---- forward -----------------------------------------------------------------
+
+template <int X, int L, int V, bool LOAD>
+__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, LoadParts q, int32_t normalize, int32_t one) {
+    constexpr int TEAMS = kThreads / L, N = kVec<X>, J = V / N, EMAX = L * V;
+    // while tokens are routed: the candidates of each team; then the wavefronts' sums; then what ends the load
+    constexpr size_t LISTS = sizeof(uint64_t) * TEAMS * EMAX, COLS = sizeof(float) * kWaves * EMAX;
+    constexpr size_t MORE = LOAD ? (COLS > sizeof(EndScratch) ? COLS : sizeof(EndScratch)) : 0;
+    __shared__ __align__(16) char pool[LISTS > MORE ? LISTS : MORE];
+    __shared__ int32_t hist[LOAD ? EMAX : 1];
+    __shared__ float slots[TEAMS][EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK];
+    const int E = la.E, k = la.k, team = threadIdx.x / L;
+    const Lane<X, L, V> lane(E);
+    const int ln = lane.ln;
+    const int64_t w = blockIdx.x / (uint32_t)q.parts, part = blockIdx.x % (uint32_t)q.parts;
+    const int64_t end = (w + 1) * a.per_worker, step = (int64_t)q.parts * TEAMS;
+    int64_t t = w * a.per_worker + part * TEAMS + team;
+    float acc[LOAD ? V : 1];
+    double squares = 0.0;
+    int tokens = 0;
+    if constexpr (LOAD) {
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int e = i * 64 + lane;
-            const float l = e < E && !masked ? load_one<X>(row + (uint64_t)e * kSize<X>) : -INFINITY;
-            any = l != l ? INFINITY : fmaxf(any, l);
-            p[i] = l == -INFINITY && lse == lse ? 0.f : expf(l - lse);
-            h[i] = slope && e < E ? a.balance * slope[e] : 0.f;
-            direct[i] = 0.f;
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        for (int e = threadIdx.x; e < EMAX; e += kThreads) hist[e] = 0;
+        __syncthreads();
+    }
+    Raw<X, N> next[J];
+    bool next_present = false;
+    auto load = [&](int64_t t) {
+        next_present = !a.mask || a.mask[t];
+        lane.load(next, reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx));
+    };
+    if (t < end) load(t);
+    for (; t < end; t += step) {
+        float l[V], p[V];
+        lane.widen(next, l, next_present);
+        if (t + step < end) load(t + step);
+        float top = l[0], sum = 0.f;
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+        top = team_max<L>(top);
+        const float from = top == -INFINITY ? 0.f : top;      // then all are -infinity (p = 0) or NaN
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = __builtin_amdgcn_exp2f((l[i] - from) * kLog2e);
+            sum += p[i];
         }
-        const bool absent = wave_max(any) == -INFINITY;
-        float inner = 0.f;
-        if (a.dgates && !absent) {
-            if (normalize)
-                for (int j = 0; j < k; ++j) inner = fmaf(a.r.gates[t * k + j], a.dgates[t * k + j], inner);
-            for (int j = 0; j < k; ++j) {
-                const int at = a.r.experts[t * k + j];
+        sum = team_sum<L>(sum);
+        const bool absent = sum == 0.f;
+        const float inv = absent ? 0.f : 1.f / sum, lse = absent ? 0.f : top + logf(sum);
+        if constexpr (LOAD) {
 #pragma unroll
-                for (int i = 0; i < kMost; ++i) {
-                    if (i * 64 + lane != at) continue;
-                    if (normalize) direct[i] = fmaf(a.r.gates[t * k + j], a.dgates[t * k + j] - inner, direct[i]);
-                    else h[i] += a.dgates[t * k + j];
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
+            if (ln == 0 && !absent) {
+                squares = fma((double)lse, (double)lse, squares);
+                ++tokens;
+            }
+        }
+        if (a.r.lse && ln == 0) a.r.lse[t] = lse;
+        int32_t* experts = a.r.experts + t * k;
+        float* gates = a.r.gates ? a.r.gates + t * k : nullptr;
+        uint64_t* list = reinterpret_cast<uint64_t*>(pool) + team * EMAX;
+        int found = k;
+        if (a.select) {
+            // k times the largest of the lanes' own maxima below the last one: at least k logits are not below it
+            float bound = INFINITY;
+            if (k <= L) {
+                float mine = l[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i) mine = fmaxf(mine, l[i]);
+                for (int j = 0; j < k; ++j) bound = team_max<L>(mine < bound ? mine : -INFINITY);
+            } else {
+                for (int j = 0; j < k; ++j) {
+                    float mine = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) mine = fmaxf(mine, l[i] < bound ? l[i] : -INFINITY);
+                    bound = team_max<L>(mine);
                 }
             }
+            bound = fmaxf(bound, -3.402823466e38f);
+            int count = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) count += l[i] >= bound ? 1 : 0;
+            int at = team_before<L>(count);
+            found = __shfl(at + count, L - 1, L);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (l[i] >= bound) list[at++] = key_of(l[i], lane.column(i));
         }
+        wave_fence();
+        float chosen = 0.f;
+        for (int c = ln; c < found; c += L) {
+            int rank = c, at = -1;
+            float g = 0.f;
+            if (a.select) {
+                const uint64_t key = list[c];
+                rank = 0;
+                for (int j = 0; j < found; ++j) rank += list[j] > key ? 1 : 0;
+                if (rank >= k) continue;
+                at = (int)~(uint32_t)key;
+                g = __builtin_amdgcn_exp2f((value_of(key) - from) * kLog2e);
+                experts[rank] = at;
+            } else {
+                at = experts[c];
+                if (at < 0 || at >= E) at = -1;
+                if (at >= 0 && !absent) {
+                    const float x = load_one<X>(reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx + at * kSize<X>));
+                    g = __builtin_amdgcn_exp2f((x - from) * kLog2e);
+                }
+            }
+            slots[team][rank] = g;
+            if (LOAD && at >= 0 && !absent) atomicAdd(&hist[at], 1);
+        }
+        if (a.select) {
+            for (int j = found + ln; j < k; j += L) {
+                slots[team][j] = 0.f;
+                experts[j] = -1;
+            }
+        }
+        wave_fence();
+        if (gates) {
+            float by = inv;
+            if (normalize && !absent) {
+                for (int j = 0; j < k; ++j) chosen += slots[team][j];
+                by = sum != sum ? sum : chosen == 0.f ? 0.f : 1.f / chosen;
+            }
+            for (int j = ln; j < k; j += L) gates[j] = absent ? 0.f : slots[team][j] * by;
+        }
+        wave_fence();
+    }
+    if constexpr (LOAD) {
+        // the wavefront's teams, then the wavefronts, in order
+        float(*cols)[EMAX] = reinterpret_cast<float(*)[EMAX]>(pool);
+        __shared__ double sq[kWaves];
+        __shared__ int32_t tok[kWaves];
+        const int wave = threadIdx.x >> 6;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int o = L; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
+            if ((threadIdx.x & 63) < L) cols[wave][lane.column(i)] = acc[i];
+        }
+        squares = wave_sum_f64(squares);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) tokens += __shfl_xor(tokens, o, 64);
+        if ((threadIdx.x & 63) == 0) {
+            sq[wave] = squares;
+            tok[wave] = tokens;
+        }
+        __syncthreads();
+        const int64_t row = blockIdx.x;
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            float s = cols[0][e];
+#pragma unroll
+            for (int j = 1; j < kWaves; ++j) s += cols[j][e];
+            q.probs[row * E + e] = s;
+            q.counts[row * E + e] = hist[e];
+        }
+        if (threadIdx.x == 0) {
+            double s = sq[0];
+            int n = tok[0];
+            for (int j = 1; j < kWaves; ++j) {
+                s += sq[j];
+                n += tok[j];
+            }
+            q.squares[row] = s;
+            q.tokens[row] = n;
+        }
+        if (!one) return;
+        if (!last_of(q.done + 1, gridDim.x)) return;
+        EndScratch& end_scratch = *reinterpret_cast<EndScratch*>(pool);
+        sum_tokens<kThreads>(la, q, end_scratch);
+        end_rest<kThreads>(la, q, end_scratch);
+        double loss = 0.0;
+        for (int c = 0; c * kChunk < E; ++c) loss += end_chunk<kThreads>(la, q, end_scratch, c);
+        if (threadIdx.x == 0) la.load.loss[0] = (float)loss;
+    }
+}
+
+// ---- backward ----------------------------------------------------------------
+
+template <int X, int L, int V>
+__global__ __launch_bounds__(kThreads) void k_route_bwd(RouteArgs a, LossArgs la, int32_t normalize, int32_t parts) {
+    constexpr int TEAMS = kThreads / L, N = kVec<X>, J = V / N, EMAX = L * V;
+    constexpr int SLOTS = (EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK) > L ? (EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK) / L : 1;
+    __shared__ __align__(16) float extra[TEAMS][EMAX];
+    const int E = la.E, k = la.k, team = threadIdx.x / L;
+    const Lane<X, L, V> lane(E);
+    const int ln = lane.ln;
+    const int64_t w = blockIdx.x / (uint32_t)parts, part = blockIdx.x % (uint32_t)parts;
+    const int64_t end = (w + 1) * a.per_worker, step = (int64_t)parts * TEAMS;
+    int64_t t = w * a.per_worker + part * TEAMS + team;
+    const float* slope = a.slope ? a.slope + (la.scope == GA_BALANCE_ALL ? 0 : w * (E + 1)) : nullptr;
+    float push[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) push[i] = slope && lane.column(i) < E ? a.balance * slope[lane.column(i)] : 0.f;
+    const float zfactor = slope ? a.z * slope[E] : 0.f;
+    if (a.dgates) {
+        for (int i = threadIdx.x; i < TEAMS * EMAX; i += kThreads) (&extra[0][0])[i] = 0.f;
+        __syncthreads();
+    }
+    Raw<X, N> next[J];
+    bool next_present = false;
+    float next_lse = 0.f;
+    auto load = [&](int64_t t) {
+        next_present = !a.mask || a.mask[t];
+        next_lse = a.r.lse[t];
+        lane.load(next, reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx));
+    };
+    if (t < end) load(t);
+    for (; t < end; t += step) {
+        float l[V], h[V], direct[V];
+        bool present = next_present;
+        const float lse = present ? next_lse : 0.f;
+        lane.widen(next, l, present);
+        // of the slots j = s * L + ln: the expert, and the gate's gradient
+        int at[SLOTS];
+        float g[SLOTS], inner = 0.f;
+        if (a.dgates) {
+            if (lse == 0.f) {       // perhaps of a token without an expert
+                float top = l[0];
+                bool nan = l[0] != l[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i) {
+                    top = fmaxf(top, l[i]);
+                    nan |= l[i] != l[i];
+                }
+                present = team_max<L>(nan ? INFINITY : top) > -INFINITY;
+            }
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) {
+                const int j = s * L + ln;
+                at[s] = -1;
+                g[s] = 0.f;
+                if (j < k && present) {
+                    at[s] = a.r.experts[t * k + j];
+                    if (at[s] < 0 || at[s] >= E) at[s] = -1;
+                    if (at[s] >= 0) g[s] = a.dgates[t * k + j];
+                }
+            }
+            if (normalize) {
+                float gate[SLOTS];
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s) {
+                    gate[s] = at[s] >= 0 ? a.r.gates[t * k + s * L + ln] : 0.f;
+                    inner = fmaf(gate[s], g[s], inner);
+                }
+                inner = team_sum<L>(inner);
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s) g[s] = gate[s] * (g[s] - inner);
+            }
+            // one slot after the other, so that the same expert twice adds up in their order
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) {
+                const int many = k - s * L < L ? k - s * L : L;
+                for (int j = 0; j < many; ++j)
+                    if (ln == j && at[s] >= 0) atomicAdd(&extra[team][at[s]], g[s]);
+            }
+            wave_fence();
+        }
+        if (t + step < end) load(t + step);
         float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < kMost; ++i)
-            if (i * 64 + lane < E) dot = fmaf(h[i], p[i], dot);
-        dot = lanes_sum_f32<64>(dot);
-        const float shift = (slope ? a.z * slope[E] * lse : 0.f) - dot;
+        for (int i = 0; i < V; ++i) {
+            const float add = a.dgates ? extra[team][lane.column(i)] : 0.f;
+            h[i] = normalize ? push[i] : push[i] + add;
+            direct[i] = normalize ? add : 0.f;
+            l[i] = __builtin_amdgcn_exp2f((l[i] - lse) * kLog2e);
+            dot = fmaf(h[i], l[i], dot);
+        }
+        if (a.dgates) {
+            wave_fence();
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int e = i * 64 + lane;
-            if (e < E) store_one<X>(out + (uint64_t)e * kSize<X>, absent ? 0.f : fmaf(p[i], h[i] + shift, direct[i]));
+            for (int s = 0; s < SLOTS; ++s)
+                if (at[s] >= 0) extra[team][at[s]] = 0.f;
+            wave_fence();
+        }
+        const float shift = fmaf(zfactor, lse, -team_sum<L>(dot));
+        const uint64_t out = reinterpret_cast<uint64_t>(a.dx) + (uint64_t)(t * a.ldd);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float d[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int i = j * N + e;
+                d[e] = present ? fmaf(l[i], h[i] + shift, direct[i]) : 0.f;
+            }
+            store_part<X>(d, out, (j * L + ln) * N, E);
         }
     }
 }
 
-template <int X>
-hipError_t router_fwd(const Router& r, const RouteArgs& a, hipStream_t s) {
-    if (a.T > 0) {
-        hipLaunchKernelGGL(k_route<X>, dim3((unsigned)(a.T < 65536 ? a.T : 65536)), dim3(64), 0, s, a, r.E, r.k, r.normalize);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+// ---- on the host -------------------------------------------------------------
+
+// Calls f with the lanes of a team and the elements of a lane.
+template <int X, typename F>
+hipError_t with_team(int E, F f) {
+#define GA_TEAM(L, V) \
+    if (E <= L * V) return f(std::integral_constant<int, L>{}, std::integral_constant<int, V>{})
+    if constexpr (X == kF32) {
+        GA_TEAM(1, 4);
+        GA_TEAM(2, 4);
+        GA_TEAM(4, 4);
+        GA_TEAM(8, 4);
+        GA_TEAM(16, 4);
+    } else {
+        GA_TEAM(1, 8);
+        GA_TEAM(2, 8);
+        GA_TEAM(4, 8);
+        GA_TEAM(8, 8);
     }
-    if (!a.with_load) return hipSuccess;
-    hipLaunchKernelGGL(k_load<X>, dim3((unsigned)r.W), dim3(256), 0, s, a, r.E, r.k, r.d_squares);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_loss, dim3(1), dim3(64), 0, s, a, r.E, r.k, r.W, r.scope, r.d_squares);
-    return hipGetLastError();
+    GA_TEAM(16, 8);
+    GA_TEAM(16, 16);
+    GA_TEAM(32, 16);
+    GA_TEAM(64, 16);
+#undef GA_TEAM
+    return hipErrorInvalidValue;
+}
+
+int64_t parts_of(int64_t tokens, int teams, int64_t most) {
+    int64_t p = (tokens + teams - 1) / teams;
+    if (p > most) p = most;
+    return p < 1 ? 1 : p;
+}
+
+// Up to this many elements of partial loads the workgroup that ends last adds them itself.
+constexpr int64_t kOneLaunch = 8192;
+
+template <int X>
+hipError_t router_fwd(const Router& r, const RouteArgs& args, hipStream_t s) {
+    RouteArgs a = args;
+    const LossArgs la = {a.load, r.E, r.k, r.W, r.scope};
+    LoadParts q = {r.d_probs, r.d_counts, r.d_squares, r.d_tokens, r.d_dots, r.d_done, 1};
+    return with_team<X>(r.E, [&](auto lanes, auto each) {
+        constexpr int L = decltype(lanes)::value, V = decltype(each)::value, TEAMS = kThreads / L;
+        if (!a.with_load) {
+            a.per_worker = a.T;
+            q.parts = (int32_t)parts_of(a.T, TEAMS, 2048);
+            hipLaunchKernelGGL((k_route<X, L, V, false>), dim3((unsigned)q.parts), dim3(kThreads), 0, s, a, la, q, r.normalize,
+                               0);
+            return hipGetLastError();
+        }
+        q.parts = (int32_t)parts_of(a.per_worker, TEAMS, r.rows / r.W);
+        const int64_t rows = (int64_t)r.W * q.parts;
+        const bool one = rows * r.E <= kOneLaunch;
+        hipLaunchKernelGGL((k_route<X, L, V, true>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, la, q, r.normalize,
+                           one ? 1 : 0);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || one) return e;
+        hipLaunchKernelGGL(k_load_end, dim3((unsigned)((r.E + kChunk - 1) / kChunk)), dim3(kEndThreads), 0, s, la, q);
+        return hipGetLastError();
+    });
 }
 
 template <int X>
-hipError_t router_bwd(const Router& r, const RouteArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_route_bwd<X>, dim3((unsigned)(a.T < 65536 ? a.T : 65536)), dim3(64), 0, s, a, r.E, r.k, r.normalize,
-                       r.scope == GA_BALANCE_ALL ? 1 : r.W, r.scope == GA_BALANCE_ALL ? a.T : a.per_worker);
-    return hipGetLastError();
+hipError_t router_bwd(const Router& r, const RouteArgs& args, hipStream_t s) {
+    RouteArgs a = args;
+    const LossArgs la = {a.load, r.E, r.k, r.W, r.scope};
+    return with_team<X>(r.E, [&](auto lanes, auto each) {
+        constexpr int L = decltype(lanes)::value, V = decltype(each)::value, TEAMS = kThreads / L;
+        int64_t workers = r.W;
+        if (r.scope == GA_BALANCE_ALL) {
+            a.per_worker = a.T;
+            workers = 1;
+        }
+        const int64_t parts = parts_of(a.per_worker, TEAMS, 1024 / workers);
+        hipLaunchKernelGGL((k_route_bwd<X, L, V>), dim3((unsigned)(workers * parts)), dim3(kThreads), 0, s, a, la, r.normalize,
+                           (int32_t)parts);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace
 
 hipError_t launch_router_fwd(const Router& r, const RouteArgs& a, hipStream_t s) {
     if (r.x_dtype == GA_FP32) return router_fwd<kF32>(r, a, s);
-    if (r.x_dtype == GA_FP16) return router_fwd<kF16>(r, a, s);
-    return router_fwd<kB16>(r, a, s);
+    return r.x_dtype == GA_FP16 ? router_fwd<kF16>(r, a, s) : router_fwd<kB16>(r, a, s);
 }
 
 hipError_t launch_router_bwd(const Router& r, const RouteArgs& a, hipStream_t s) {
     if (r.x_dtype == GA_FP32) return router_bwd<kF32>(r, a, s);
-    if (r.x_dtype == GA_FP16) return router_bwd<kF16>(r, a, s);
-    return router_bwd<kB16>(r, a, s);
+    return r.x_dtype == GA_FP16 ? router_bwd<kF16>(r, a, s) : router_bwd<kB16>(r, a, s);
 }
 
 }  // namespace ga
