@@ -1,8 +1,8 @@
 // Group norm forward, with its activation (ga_groupnorm_forward).
 //
 // The statistics of a group take one pass: each thread sums the deviations from a
-// value of its own (shift: it reads that value first, so that an outlier there is
-// among its squares too) and their squares as its vectors arrive.  The sums of all
+// value of its own (shift, the mean of its first vector: an outlier there is among
+// its squares too) and their squares as its vectors arrive.  The sums of all
 // threads give the mean m; with d = m - shift a thread's squares about m are
 // s2 - 2 d s1 + count d^2, and its deviations from m, s1 - count d, add up to what
 // m's roundings left, which corrects it.
@@ -12,9 +12,9 @@ namespace ga {
 
 namespace {
 
-template <bool WHOLE, int N>
+template <int MODE, int N>
 struct Moments {
-    static constexpr int M = WHOLE ? 1 : N;    // a sum of the vector, or one for each channel
+    static constexpr int M = MODE == kWhole ? 1 : N;    // a sum of the vector, or one for each channel
     float shift[M], s1[M], s2[M];
     int rows;
 
@@ -23,26 +23,43 @@ struct Moments {
         for (int e = 0; e < M; ++e) shift[e] = s1[e] = s2[e] = 0.f;
     }
 
-    __device__ __forceinline__ void add(float (&f)[N], const Place<WHOLE, N>& p) {
-        const bool full = p.left >= N;
-        if (rows++ == 0) {
-            if constexpr (!WHOLE) {
+    template <bool RAGGED>
+    __device__ __forceinline__ void start(const float (&f)[N], const Place<MODE, N>& p) {
+        if constexpr (MODE == kWhole) {
+            const bool full = !RAGGED || p.left >= N;
+            float t = 0.f;
 #pragma unroll
-                for (int e = 0; e < N; ++e) shift[e] = f[e];
-            } else {
-                float t = 0.f;
+            for (int e = 0; e < N; ++e) t += full || e < p.left ? f[e] : 0.f;
+            shift[0] = t * (full ? 1.f / N : 1.f / (float)p.left);
+        } else if constexpr (MODE == kSpan) {
+            // of the vector's two groups each its own
+            const int left = RAGGED && p.left < N ? p.left : N, border = p.border < left ? p.border : left;
+            float first = 0.f, second = 0.f;
 #pragma unroll
-                for (int e = 0; e < N; ++e) t += full || e < p.left ? f[e] : 0.f;
-                shift[0] = t * (full ? 1.f / N : 1.f / (float)p.left);
+            for (int e = 0; e < N; ++e) {
+                first += e < border ? f[e] : 0.f;
+                second += e >= border && e < left ? f[e] : 0.f;
             }
+            first *= 1.f / (float)border;
+            second *= left > border ? 1.f / (float)(left - border) : 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) shift[e] = e < border ? first : second;
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) shift[e] = f[e];
         }
-        if (WHOLE && !full) {
+    }
+
+    template <bool RAGGED>
+    __device__ __forceinline__ void add(float (&f)[N], const Place<MODE, N>& p) {
+        ++rows;
+        if (MODE == kWhole && RAGGED && p.left < N) {
 #pragma unroll
             for (int e = 0; e < N; ++e) f[e] = e < p.left ? f[e] : shift[0];
         }
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const int k = WHOLE ? 0 : e;
+            const int k = MODE == kWhole ? 0 : e;
             const float d = f[e] - shift[k];
             s1[k] += d;
             s2[k] = fmaf(d, d, s2[k]);
@@ -51,93 +68,166 @@ struct Moments {
 };
 
 // What a thread's groups have over all of a workgroup's values: m, the mean as first rounded; off, the mean of the
-// deviations from it; sq, the sum of their squares (not yet less count * off^2).  base: a value of the group, or one
-// that its threads share; constant groups add up exactly about it.
-template <bool WHOLE, int N, int T>
-__device__ __forceinline__ void statistics(const Moments<WHOLE, N>& t, float base, float inv, float (&m)[WHOLE ? 1 : N],
-                                           float (&off)[WHOLE ? 1 : N], float (&sq)[WHOLE ? 1 : N], float* tile, float* res,
-                                           const GnShape& h, const Place<WHOLE, N>& p) {
-    constexpr int M = WHOLE ? 1 : N;
+// deviations from it; sq, the sum of their squares (not yet less count * off^2).  Constant groups add up exactly.
+template <int MODE, int N, int T>
+__device__ __forceinline__ void statistics(const Moments<MODE, N>& t, float base, float inv, float (&m)[Moments<MODE, N>::M],
+                                           float (&off)[Moments<MODE, N>::M], float (&sq)[Moments<MODE, N>::M], float* lds,
+                                           const GnShape& h, const Place<MODE, N>& p) {
+    constexpr int M = Moments<MODE, N>::M, SEGMENTS = MODE == kSpan ? 2 : 1;
     const int all = h.Q * h.sg;
-    const float count = (float)t.rows * (float)(!WHOLE ? 1 : p.left >= N ? N : p.left > 0 ? p.left : 0);
-    int at[M];
-    float first[1][M], d1[1][M], d2[1][M];
+    if constexpr (MODE != kMany) {
+        // s1, s2, shift and count of each thread and group; a group's teams of threads read them twice
+        f32x4* tile = reinterpret_cast<f32x4*>(lds);
+        float* res = lds + SEGMENTS * 4 * T;
+        if constexpr (MODE == kWhole) {
+            const int mine = p.left >= N ? N : p.left > 0 ? p.left : 0;
+            tile[threadIdx.x] = f32x4{t.s1[0], t.s2[0], t.shift[0], (float)t.rows * (float)mine};
+        } else {
+            f32x4 first = {0.f, 0.f, t.shift[0], 0.f}, second = {0.f, 0.f, t.shift[N - 1], 0.f};
+            const int left = p.left < N ? p.left : N, border = p.border < left ? p.border : left;
 #pragma unroll
-    for (int e = 0; e < M; ++e) {
-        at[e] = p.here ? p.q * h.sg + p.group(h, e) : 0;
-        first[0][e] = t.rows ? fmaf(count, t.shift[e] - base, t.s1[e]) : 0.f;
-    }
-    sum_groups<WHOLE, N, T, 1>(first, tile, res, h, p);
+            for (int e = 0; e < N; ++e) {
+                first.x += e < border ? t.s1[e] : 0.f;
+                first.y += e < border ? t.s2[e] : 0.f;
+                second.x += e >= border && e < left ? t.s1[e] : 0.f;
+                second.y += e >= border && e < left ? t.s2[e] : 0.f;
+            }
+            first.w = (float)t.rows * (float)(border > 0 ? border : 0);
+            second.w = (float)t.rows * (float)(left > border ? left - border : 0);
+            tile[threadIdx.x] = first;
+            tile[T + threadIdx.x] = second;
+        }
+        __syncthreads();
+        const int j = threadIdx.x & (h.lanes - 1), jv = j & (h.spread - 1), jr = j / h.spread, rows = h.lanes / h.spread;
+        for (int vg = threadIdx.x / h.lanes; vg < all; vg += T / h.lanes) {
+            const int q = h.Q == 1 ? 0 : vg / h.sg, g = vg - q * h.sg, c0 = g * h.cg;
+            const int v0 = h.sg == 1 ? 0 : c0 / N, v1 = h.sg == 1 ? h.nv - 1 : (c0 + h.cg - 1) / N;
+            // vectors that start before the group have it as their second
+            const f32x4* of = tile + q * h.R * h.nv;
+            auto entry = [&](int r, int v) { return of[(MODE == kSpan && v * N < c0 ? T : 0) + r * h.nv + v]; };
+            const float about = entry(0, v0).z;
+            float s[1] = {0.f}, u[2] = {0.f, 0.f};
+            for (int r = jr; r < h.R; r += rows) {
+                for (int v = v0 + jv; v <= v1; v += h.spread) {
+                    const f32x4 a = entry(r, v);
+                    s[0] += fmaf(a.w, a.z - about, a.x);
+                }
+            }
+            sum_lanes(s, h.lanes);
+            const float mean = fmaf(s[0], inv, about);
+            for (int r = jr; r < h.R; r += rows) {
+                for (int v = v0 + jv; v <= v1; v += h.spread) {
+                    const f32x4 a = entry(r, v);
+                    const float d = mean - a.z, dev = fmaf(-a.w, d, a.x);
+                    u[0] += dev;
+                    u[1] += fmaf(-d, a.x + dev, a.y);         // s2 - 2 d s1 + count d^2
+                }
+            }
+            sum_lanes(u, h.lanes);
+            if (j == 0) {
+                res[vg] = mean;
+                res[all + vg] = u[0] * inv;
+                res[2 * all + vg] = u[1];
+            }
+        }
+        __syncthreads();
 #pragma unroll
-    for (int e = 0; e < M; ++e) {
-        m[e] = fmaf(res[at[e]], inv, base);
-        const float d = m[e] - t.shift[e];
-        d1[0][e] = t.rows ? fmaf(-count, d, t.s1[e]) : 0.f;
-        d2[0][e] = t.rows ? fmaf(-d, t.s1[e] + d1[0][e], t.s2[e]) : 0.f;
-    }
-    if constexpr (WHOLE) {
-        const float both[2][1] = {{d1[0][0]}, {d2[0][0]}};
-        sum_groups<WHOLE, N, T, 2>(both, tile, res + all, h, p);
+        for (int e = 0; e < M; ++e) {
+            const int at = p.here ? p.q * h.sg + p.group(h, e) : 0;
+            m[e] = res[at];
+            off[e] = res[all + at];
+            sq[e] = res[2 * all + at];
+        }
     } else {
-        sum_groups<WHOLE, N, T, 1>(d1, tile, res + all, h, p);
-        sum_groups<WHOLE, N, T, 1>(d2, tile, res + 2 * all, h, p);
-    }
+        float *tile = lds, *res = lds + T * N + h.slices * h.Q * h.nv * N;
+        const float count = (float)t.rows;
+        float x[1][M];
 #pragma unroll
-    for (int e = 0; e < M; ++e) {
-        off[e] = res[all + at[e]] * inv;
-        sq[e] = res[2 * all + at[e]];
+        for (int e = 0; e < M; ++e) x[0][e] = t.rows ? fmaf(count, t.shift[e] - base, t.s1[e]) : 0.f;
+        sum_groups<N, T>(x, tile, res, h, p);
+#pragma unroll
+        for (int e = 0; e < M; ++e) {
+            m[e] = fmaf(res[p.here ? p.q * h.sg + p.group(h, e) : 0], inv, base);
+            x[0][e] = t.rows ? fmaf(-count, m[e] - t.shift[e], t.s1[e]) : 0.f;
+        }
+        sum_groups<N, T>(x, tile, res + all, h, p);
+#pragma unroll
+        for (int e = 0; e < M; ++e) {
+            off[e] = res[all + (p.here ? p.q * h.sg + p.group(h, e) : 0)] * inv;
+            x[0][e] = t.rows ? fmaf(t.shift[e] - m[e], t.s1[e] + x[0][e], t.s2[e]) : 0.f;
+        }
+        sum_groups<N, T>(x, tile, res + 2 * all, h, p);
+#pragma unroll
+        for (int e = 0; e < M; ++e) sq[e] = res[2 * all + (p.here ? p.q * h.sg + p.group(h, e) : 0)];
     }
 }
 
-// The first value of the group (WHOLE) or of the slab; it may be another group's, and then not finite.
-template <int X, bool WHOLE, int N>
-__device__ __forceinline__ float base_value(uint64_t image, const GnShape& h, const Place<WHOLE, N>& p) {
-    const float b = load_one<X>(image + (uint64_t)((p.g0 + (WHOLE ? p.group(h, 0) : 0)) * h.cg) * kSize<X>);
+// Bytes of LDS that they take.
+size_t lds_of_statistics(GnMode mode, const GnShape& h, int N, int T) {
+    const size_t tile = mode == kWhole ? 4 * (size_t)T : mode == kSpan ? 8 * (size_t)T
+                                       : (size_t)T * N + (size_t)h.slices * h.Q * h.nv * N;
+    return sizeof(float) * (tile + 3 * (size_t)h.Q * h.sg);
+}
+
+// The slab's first value, which its threads share; it may not be finite, and another group's.
+template <int X, int MODE, int N>
+__device__ __forceinline__ float base_value(uint64_t image, const Place<MODE, N>& p) {
+    if constexpr (MODE != kMany) return 0.f;
+    const float b = load_one<X>(image + (uint64_t)p.c0 * kSize<X>);
     return fabsf(b) < INFINITY ? b : 0.f;
 }
 
 // y of one vector: (x - m) * scale + bias, activated.
-template <int X, bool WHOLE, int N>
-__device__ __forceinline__ void put_vector(const Raw<X, N>& x, const float (&m)[WHOLE ? 1 : N], const float (&scale)[N],
-                                           const float (&bias)[N], uint64_t row, const Place<WHOLE, N>& p, int32_t act) {
+template <int X, bool RAGGED, bool STREAM, int MODE, int N>
+__device__ __forceinline__ void put_vector(const Raw<X, N>& x, const float (&m)[Moments<MODE, N>::M], const float (&scale)[N],
+                                           const float (&bias)[N], uint64_t row, const Place<MODE, N>& p, const GnShape& h) {
     float f[N];
     x.widen(f);
 #pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = fmaf(f[e] - m[WHOLE ? 0 : e], scale[e], bias[e]);
-    activate(f, act);
-    store_part<X, true>(f, row, p.c, p.c + (p.left < N ? p.left : N));
+    for (int e = 0; e < N; ++e) f[e] = fmaf(f[e] - m[MODE == kWhole ? 0 : e], scale[e], bias[e]);
+    activate(f, h.act);
+    store_vector<X, RAGGED, STREAM>(f, row, p);
 }
 
 // A sample's slab that stays in registers, V vectors to a thread.
-template <int X, bool WHOLE, int T, int V>
+template <int X, int MODE, int T, int V>
 __global__ __launch_bounds__(T) void k_gn_fwd(GnArgs a, GnShape h) {
-    constexpr int N = kVec<X>, M = WHOLE ? 1 : N;
-    extern __shared__ float lds[];
-    const uint32_t id = xcd_block();
-    const Place<WHOLE, N> p(h, (int)(id % (uint32_t)h.slabs));
+    constexpr int N = kVec<X>, M = MODE == kWhole ? 1 : N;
+    extern __shared__ __align__(16) float lds[];
+    const uint32_t id = xcd_block(gridDim.x);
+    const Place<MODE, N> p(h, (int)(id % (uint32_t)h.slabs));
     const int64_t n = (int64_t)(id / (uint32_t)h.slabs) * h.Q + p.q;
     const bool in = p.here && n < a.N && p.left > 0;
-    const int rows = in ? (h.S - p.r + h.R - 1) / h.R : 0;
-    const uint64_t xr = reinterpret_cast<uint64_t>(a.x.data) + (uint64_t)(n * a.x.sample);
+    const int most = (h.S + h.R - 1) / h.R, last = p.r + (most - 1) * h.R;    // rows of a thread; its last row
+    const bool fits = last < h.S;
+    const uint64_t image = reinterpret_cast<uint64_t>(a.x.data) + (uint64_t)((n < a.N ? n : a.N - 1) * a.x.sample);
+    const uint64_t xr = image + (uint64_t)(p.r * a.x.ld), xl = image + (uint64_t)((fits ? last : h.S - 1) * a.x.ld);
+    const int64_t step = h.R * a.x.ld;
     Raw<X, N> x[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (i < rows) load_ahead<X, N, false>(x[i], xr + (uint64_t)((p.r + i * h.R) * a.x.ld), p.c, h.C);
-    const float base = in ? base_value<X>(xr, h, p) : 0.f;
+        if (i < most) load_vector<X, false>(x[i], i + 1 < most ? xr + (uint64_t)(i * step) : xl, h, p);
+    const float base = base_value<X>(image, p);
     float scale[N], bias[N];
     load_weight<X>(scale, a.gamma, h, p.c, 1.f);
     load_weight<X>(bias, a.beta, h, p.c, 0.f);
-    Moments<WHOLE, N> t;
+    Moments<MODE, N> t;
+    if (in) {
+        if_ragged(p.ragged, [&](auto ragged) {
+            constexpr bool RAGGED = decltype(ragged)::value;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (i >= rows) continue;
-        float f[N];
-        if (p.past) drop_front(x[i], p.past);
-        x[i].widen(f);
-        t.add(f, p);
+            for (int i = 0; i < V; ++i) {
+                if (i >= most) continue;
+                float f[N];
+                into_row<X, RAGGED>(x[i], p.past);
+                x[i].widen(f);
+                if (i == 0) t.template start<RAGGED>(f, p);
+                if (i + 1 < most || fits) t.template add<RAGGED>(f, p);
+            }
+        });
     }
     float m[M], off[M], sq[M];
-    statistics<WHOLE, N, T>(t, base, h.inv_n, m, off, sq, lds, lds + h.res_at, h, p);
+    statistics<MODE, N, T>(t, base, h.inv_n, m, off, sq, lds, h, p);
     if (!in) return;
 #pragma unroll
     for (int e = 0; e < M; ++e) {
@@ -152,13 +242,18 @@ __global__ __launch_bounds__(T) void k_gn_fwd(GnArgs a, GnShape h) {
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        scale[e] *= sq[WHOLE ? 0 : e];
-        bias[e] = fmaf(-off[WHOLE ? 0 : e], scale[e], bias[e]);
+        scale[e] *= sq[MODE == kWhole ? 0 : e];
+        bias[e] = fmaf(-off[MODE == kWhole ? 0 : e], scale[e], bias[e]);
     }
-    const uint64_t yr = reinterpret_cast<uint64_t>(a.y.data) + (uint64_t)(n * a.y.sample);
+    const uint64_t yr = reinterpret_cast<uint64_t>(a.y.data) + (uint64_t)(n * a.y.sample + p.r * a.y.ld);
+    const int64_t stepy = h.R * a.y.ld;
+    if_ragged(p.ragged, [&](auto ragged) {
+        constexpr bool RAGGED = decltype(ragged)::value;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i < rows) put_vector<X>(x[i], m, scale, bias, yr + (uint64_t)((p.r + i * h.R) * a.y.ld), p, h.act);
+        for (int i = 0; i < V; ++i)
+            if (i < most && (i + 1 < most || fits))
+                put_vector<X, RAGGED, false>(x[i], m, scale, bias, yr + (uint64_t)(i * stepy), p, h);
+    });
 }
 
 // ---- images that do not stay in registers ------------------------------------
@@ -167,38 +262,62 @@ __global__ __launch_bounds__(T) void k_gn_fwd(GnArgs a, GnShape h) {
 // Of a part (and piece) of a group: the mean m + off and the sum of squares about it.
 typedef f32x4 GnRecord;
 
-template <int X, bool WHOLE, int T>
+template <int X, int MODE, bool TINY, int T>
 __global__ __launch_bounds__(T) void k_gn_stats(GnArgs a, GnShape h, GnRecord* __restrict__ records) {
-    constexpr int N = kVec<X>, M = WHOLE ? 1 : N;
-    extern __shared__ float lds[];
-    const PartOf o(h, xcd_block());
-    const Place<WHOLE, N> p(h, o.slab);
-    const uint64_t xr = reinterpret_cast<uint64_t>(a.x.data) + (uint64_t)(o.n * a.x.sample);
+    constexpr int N = kVec<X>, M = MODE == kWhole ? 1 : N;
+    extern __shared__ __align__(16) float lds[];
+    const PartOf o(h, xcd_block(gridDim.x));
+    const Place<MODE, N> p(h, o.slab);
+    const uint64_t image = reinterpret_cast<uint64_t>(a.x.data) + (uint64_t)(o.n * a.x.sample);
     const bool in = p.here && p.left > 0;
-    const float base = in ? base_value<X>(xr, h, p) : 0.f;
-    Moments<WHOLE, N> t;
-    if (in) {
-        const int64_t step = h.R * a.x.ld;
-        uint64_t row = xr + (uint64_t)((int64_t)(o.s0 + p.r) * a.x.ld);
-        for (int64_t s = (int64_t)o.s0 + p.r; s < o.s1; s += kAhead * h.R, row += kAhead * step) {
-            Raw<X, N> x[kAhead];
+    const float base = base_value<X>(image, p);
+    Moments<MODE, N> t;
+    const Rows rows(h, o.part, p.r);
+    if (in && rows.full + rows.tail > 0) {
+        if_ragged(TINY || p.ragged, [&](auto ragged) {
+            constexpr bool RAGGED = decltype(ragged)::value;
+            const int64_t step = h.R * a.x.ld, stride = (int64_t)h.parts * kAhead * step;
+            uint64_t row = image + (uint64_t)(rows.first * a.x.ld);
+            Raw<X, N> x[kAhead], y[kAhead];
+            auto load = [&](Raw<X, N>(&to)[kAhead], int many) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (s + (int64_t)i * h.R < o.s1) load_ahead<X, N, false>(x[i], row + i * step, p.c, h.C);
+                for (int i = 0; i < kAhead; ++i)
+                    if (i < many) load_vector<X, TINY>(to[i], row + (uint64_t)(i * step), h, p);
+                row += (uint64_t)stride;
+            };
+            auto add = [&](Raw<X, N>(&of)[kAhead], int many, bool first) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (s + (int64_t)i * h.R >= o.s1) continue;
-                float f[N];
-                if (p.past) drop_front(x[i], p.past);
-                x[i].widen(f);
-                t.add(f, p);
+                for (int i = 0; i < kAhead; ++i) {
+                    if (i >= many) continue;
+                    float f[N];
+                    into_row<X, RAGGED>(of[i], p.past);
+                    of[i].widen(f);
+                    if (i == 0 && first) t.template start<RAGGED>(f, p);
+                    t.template add<RAGGED>(f, p);
+                }
+            };
+            // the next vectors are on their way while these are added
+            if (rows.full > 0) {
+                load(x, kAhead);
+                for (int i = 0; i + 1 < rows.full; ++i) {
+                    load(y, kAhead);
+                    add(x, kAhead, i == 0);
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) x[k] = y[k];
+                }
+                if (rows.tail > 0) load(y, rows.tail);
+                add(x, kAhead, rows.full == 1);
+                if (rows.tail > 0) add(y, rows.tail, false);
+            } else {
+                load(x, rows.tail);
+                add(x, rows.tail, true);
             }
-        }
+        });
     }
     // of the groups' values in this part and slab
-    const float count = (float)(o.s1 - o.s0) * (float)(h.pieces == 1 ? h.cg : p.channels), inv = 1.f / count;
+    const float count = (float)positions_of(h, o.part) * (float)(h.pieces == 1 ? h.cg : p.channels), inv = 1.f / count;
     float m[M], off[M], sq[M];
-    statistics<WHOLE, N, T>(t, base, inv, m, off, sq, lds, lds + h.res_at, h, p);
+    statistics<MODE, N, T>(t, base, inv, m, off, sq, lds, h, p);
     if (!in || p.r != 0) return;
     const int K = h.parts * h.pieces, k = o.part * h.pieces + (h.pieces == 1 ? 0 : o.slab % h.pieces);
 #pragma unroll
@@ -211,23 +330,26 @@ __global__ __launch_bounds__(T) void k_gn_stats(GnArgs a, GnShape h, GnRecord* _
     }
 }
 
-template <int X, bool WHOLE, int T>
+template <int X, int MODE, bool TINY, int T>
 __global__ __launch_bounds__(T) void k_gn_apply(GnArgs a, GnShape h, const GnRecord* __restrict__ records) {
-    constexpr int N = kVec<X>, M = WHOLE ? 1 : N;
-    extern __shared__ float lds[];        // m, what its rounding left, 1/deviation of the slab's groups
-    const PartOf o(h, xcd_block());
-    const Place<WHOLE, N> p(h, o.slab);
-    const uint64_t xr = reinterpret_cast<uint64_t>(a.x.data) + (uint64_t)(o.n * a.x.sample);
-    const uint64_t yr = reinterpret_cast<uint64_t>(a.y.data) + (uint64_t)(o.n * a.y.sample);
+    constexpr int N = kVec<X>, M = MODE == kWhole ? 1 : N;
+    extern __shared__ __align__(16) float lds[];        // m, what its rounding left, 1/deviation of the slab's groups
+    const PartOf o(h, xcd_block(gridDim.x));
+    const Place<MODE, N> p(h, o.slab);
     const bool in = p.here && p.left > 0;
-    const int64_t step = h.R * a.x.ld;
-    uint64_t row = xr + (uint64_t)((int64_t)(o.s0 + p.r) * a.x.ld);
-    int64_t s = (int64_t)o.s0 + p.r;
+    const Rows rows(h, o.part, p.r);
+    const int64_t step = h.R * a.x.ld, stepy = h.R * a.y.ld, ahead = (int64_t)h.parts * kAhead;
+    uint64_t row = reinterpret_cast<uint64_t>(a.x.data) + (uint64_t)(o.n * a.x.sample + rows.first * a.x.ld);
+    uint64_t yr = reinterpret_cast<uint64_t>(a.y.data) + (uint64_t)(o.n * a.y.sample + rows.first * a.y.ld);
+    int full = in ? rows.full : 0;
+    const int tail = in ? rows.tail : 0;
     Raw<X, N> x[kAhead];
-    auto load = [&]() {
+    auto load = [&]() {     // the next chunk, or the incomplete one
+        const int many = full > 0 ? kAhead : tail;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (in && s + (int64_t)i * h.R < o.s1) load_ahead<X, N, false>(x[i], row + i * step, p.c, h.C);
+            if (i < many) load_vector<X, TINY>(x[i], row + (uint64_t)(i * step), h, p);
+        row += (uint64_t)(ahead * step);
     };
     load();
     float scale[N], bias[N];
@@ -238,18 +360,16 @@ __global__ __launch_bounds__(T) void k_gn_apply(GnArgs a, GnShape h, const GnRec
         const int group = p.g0 + g < h.G ? p.g0 + g : h.G - 1;
         const GnRecord* of = records + o.n * K * h.G + group;
         auto count = [&](int k) {
-            const int part = k / h.pieces, first = (k - part * h.pieces) * h.nv * N;
-            const int rows = h.S - part * h.span < h.span ? h.S - part * h.span : h.span;
-            return (double)rows * (h.pieces == 1 ? h.cg : h.nv * N < h.cg - first ? h.nv * N : h.cg - first);
+            const int part = h.pieces == 1 ? k : k / h.pieces, first = (k - part * h.pieces) * h.nv * N;
+            return (double)positions_of(h, part) * (h.pieces == 1 ? h.cg : h.nv * N < h.cg - first ? h.nv * N : h.cg - first);
         };
-        const double inv = 1.0 / ((double)h.S * h.cg);
         double sum = 0.0, sq = 0.0;
         for (int k = j; k < K; k += h.lanes) {
             const GnRecord r = of[(int64_t)k * h.G];
             sum += count(k) * ((double)r.x + (double)r.y);
         }
         for (int b = h.lanes >> 1; b; b >>= 1) sum += __shfl_xor(sum, b, 64);
-        const double mean = sum * inv;
+        const double mean = sum * h.inv_count;
         for (int k = j; k < K; k += h.lanes) {
             const GnRecord r = of[(int64_t)k * h.G];
             const double d = (double)r.x + (double)r.y - mean;
@@ -257,7 +377,7 @@ __global__ __launch_bounds__(T) void k_gn_apply(GnArgs a, GnShape h, const GnRec
         }
         for (int b = h.lanes >> 1; b; b >>= 1) sq += __shfl_xor(sq, b, 64);
         if (j == 0) {
-            const float m = (float)mean, rstd = 1.f / sqrtf((float)(sq * inv) + a.eps);
+            const float m = (float)mean, rstd = 1.f / sqrtf((float)(sq * h.inv_count) + a.eps);
             lds[3 * g] = m;
             lds[3 * g + 1] = (float)(mean - (double)m);
             lds[3 * g + 2] = rstd;
@@ -268,7 +388,7 @@ __global__ __launch_bounds__(T) void k_gn_apply(GnArgs a, GnShape h, const GnRec
         }
     }
     __syncthreads();
-    if (!in) return;
+    if (full + tail == 0) return;
     float m[M];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -277,26 +397,36 @@ __global__ __launch_bounds__(T) void k_gn_apply(GnArgs a, GnShape h, const GnRec
         scale[e] *= lds[3 * g + 2];
         bias[e] = fmaf(-lds[3 * g + 1], scale[e], bias[e]);
     }
-    for (; s < o.s1; ) {
-        const int64_t now = s;
-        Raw<X, N> y[kAhead];
+    auto all = [&](auto ragged, auto stream) {
+        constexpr bool RAGGED = decltype(ragged)::value, STREAM = decltype(stream)::value;
+        auto put = [&](Raw<X, N>& v, int i) {
+            into_row<X, RAGGED>(v, p.past);
+            put_vector<X, RAGGED, STREAM>(v, m, scale, bias, yr + (uint64_t)(i * stepy), p, h);
+        };
+        while (full > 0) {
+            Raw<X, N> now[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) y[i] = x[i];
-        s += kAhead * h.R;
-        row += kAhead * step;
-        load();
+            for (int i = 0; i < kAhead; ++i) now[i] = x[i];
+            --full;
+            load();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (now + (int64_t)i * h.R >= o.s1) continue;
-            if (p.past) drop_front(y[i], p.past);
-            put_vector<X>(y[i], m, scale, bias, yr + (uint64_t)((now + (int64_t)i * h.R) * a.y.ld), p, h.act);
+            for (int i = 0; i < kAhead; ++i) put(now[i], i);
+            yr += (uint64_t)(ahead * stepy);
         }
-    }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < tail) put(x[i], i);
+    };
+    const std::integral_constant<bool, true> yes;
+    const std::integral_constant<bool, false> no;
+    if (TINY || p.ragged) all(yes, no);
+    else if (h.stream) all(no, yes);
+    else all(no, no);
 }
 
 // ---- on the host -------------------------------------------------------------
 
-constexpr TeamSize kTeams[] = {{256, 1}, {256, 2}, {256, 4}, {512, 4}, {512, 8}, {1024, 8}, {1024, 16}};
+constexpr TeamSize kTeams[] = {{256, 1}, {256, 2}, {256, 4}, {512, 4}, {512, 8}};
 
 // Calls f with the team's sizes as constants.
 template <typename F>
@@ -307,13 +437,11 @@ hipError_t with_team(int k, F f) {
     GA_TEAM(2);
     GA_TEAM(3);
     GA_TEAM(4);
-    GA_TEAM(5);
-    GA_TEAM(6);
 #undef GA_TEAM
     return hipErrorInvalidValue;
 }
 
-constexpr int kWideThreads = 512;
+constexpr int kWideThreads = 256;
 
 // The arguments of samples [n0, n0 + count).
 GnArgs samples_of(const GnArgs& all, int32_t G, int64_t n0, int64_t count) {
@@ -330,19 +458,19 @@ template <int X>
 hipError_t gn_fwd(const GroupNorm& n, const GnArgs& all, hipStream_t s) {
     constexpr int N = kVec<X>;
     GnShape h = shape_of(n, all.S);
-    const int k = choose(h, N, kTeams, all.N);
+    const int k = choose(h, N, kTeams, 4, all.N);
     if (k >= 0) {
-        const bool whole = whole_vectors(h, N);
-        h.res_at = (int32_t)lds_of_groups(h, N, kTeams[k].T, whole ? 2 : 1);
-        const size_t bytes = sizeof(float) * ((size_t)h.res_at + 3 * (size_t)h.Q * h.sg);
+        const GnMode mode = mode_of(h, N);
+        const size_t bytes = lds_of_statistics(mode, h, N, kTeams[k].T);
         const int64_t step = kMostBlocks / h.slabs * h.Q;
         for (int64_t n0 = 0; n0 < all.N; n0 += step) {
             const GnArgs a = samples_of(all, n.G, n0, all.N - n0 < step ? all.N - n0 : step);
             const unsigned blocks = (unsigned)(ceil_div(a.N, h.Q) * h.slabs);
             const hipError_t e = with_team(k, [&](auto t, auto v) {
                 constexpr int T = decltype(t)::value, V = decltype(v)::value;
-                if (whole) hipLaunchKernelGGL((k_gn_fwd<X, true, T, V>), dim3(blocks), dim3(T), bytes, s, a, h);
-                else hipLaunchKernelGGL((k_gn_fwd<X, false, T, V>), dim3(blocks), dim3(T), bytes, s, a, h);
+                with_mode(mode, [&](auto m) {
+                    hipLaunchKernelGGL((k_gn_fwd<X, decltype(m)::value, T, V>), dim3(blocks), dim3(T), bytes, s, a, h);
+                });
                 return hipGetLastError();
             });
             if (e != hipSuccess) return e;
@@ -350,10 +478,11 @@ hipError_t gn_fwd(const GroupNorm& n, const GnArgs& all, hipStream_t s) {
         return hipSuccess;
     }
     constexpr int T = kWideThreads;
-    lay_wide(h, N, T, all.N, 1024);
-    const bool whole = whole_vectors(h, N);
-    h.res_at = (int32_t)lds_of_groups(h, N, T, whole ? 2 : 1);
-    const size_t bytes = sizeof(float) * ((size_t)h.res_at + 3 * (size_t)h.sg);
+    lay_wide(h, N, T, all.N);
+    h.stream = whole_lines(h, all.y, kSize<X>);
+    const bool tiny = h.C < N;
+    const GnMode mode = tiny ? kMany : mode_of(h, N);
+    const size_t bytes = lds_of_statistics(mode, h, N, T);
     // as many samples at once as the records have room for
     const int64_t per = (int64_t)h.parts * h.pieces * n.G;
     int64_t step = kGnRecords / per;
@@ -363,13 +492,15 @@ hipError_t gn_fwd(const GroupNorm& n, const GnArgs& all, hipStream_t s) {
         const GnArgs a = samples_of(all, n.G, n0, all.N - n0 < step ? all.N - n0 : step);
         const unsigned blocks = (unsigned)(a.N * h.parts * h.slabs);
         GnRecord* records = reinterpret_cast<GnRecord*>(n.d_records);
-        if (whole) {
-            hipLaunchKernelGGL((k_gn_stats<X, true, T>), dim3(blocks), dim3(T), bytes, s, a, h, records);
-            hipLaunchKernelGGL((k_gn_apply<X, true, T>), dim3(blocks), dim3(T), bytes, s, a, h, records);
-        } else {
-            hipLaunchKernelGGL((k_gn_stats<X, false, T>), dim3(blocks), dim3(T), bytes, s, a, h, records);
-            hipLaunchKernelGGL((k_gn_apply<X, false, T>), dim3(blocks), dim3(T), bytes, s, a, h, records);
-        }
+        auto launch = [&](auto m, auto t) {
+            constexpr int MODE = decltype(m)::value;
+            constexpr bool TINY = decltype(t)::value;
+            hipLaunchKernelGGL((k_gn_stats<X, MODE, TINY, T>), dim3(blocks), dim3(T), bytes, s, a, h, records);
+            hipLaunchKernelGGL((k_gn_apply<X, MODE, TINY, T>), dim3(blocks), dim3(T), sizeof(float) * 3 * h.sg, s, a, h,
+                               records);
+        };
+        if (tiny) launch(std::integral_constant<int, kMany>{}, std::integral_constant<bool, true>{});
+        else with_mode(mode, [&](auto m) { launch(m, std::integral_constant<bool, false>{}); });
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
