@@ -9,7 +9,7 @@ namespace ga {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504f;
 
@@ -108,6 +108,28 @@ __device__ __forceinline__ float value_of(uint64_t key) {
     return __uint_as_float(u ^ ((int32_t)u < 0 ? 0x80000000u : 0xffffffffu));
 }
 
+// Of the maxima of the team's L * GROUPS groups of logits (a lane's V are GROUPS of them), the k-th when equal ones count
+// once; -infinity where there are fewer.
+template <int L, int V, int GROUPS>
+__device__ __forceinline__ float kth_of_groups(const float (&l)[V], int k) {
+    constexpr int EACH = V / GROUPS;
+    float top[GROUPS];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        top[g] = l[g * EACH];
+#pragma unroll
+        for (int i = 1; i < EACH; ++i) top[g] = fmaxf(top[g], l[g * EACH + i]);
+    }
+    float bound = INFINITY;
+    for (int j = 0; j < k; ++j) {
+        float best = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) best = fmaxf(best, top[g] < bound || j == 0 ? top[g] : -INFINITY);
+        bound = team_max<L>(best);
+    }
+    return bound;
+}
+
 // Where the partial loads of the workgroups lie: row = worker * parts + part.
 struct LoadParts {
     float* probs;          // [rows][E]
@@ -126,72 +148,61 @@ struct LossArgs {
     int32_t E, k, W, scope;
 };
 
-// Ends the load of chunk `chunk` of the experts: the workers' counts and sums, and the slope; returns the chunk's part
-// of the balance loss in thread 0.  THREADS threads, of which kChunk share an expert's row each.
+template <int THREADS>
 struct EndScratch {
-    double p[64][kChunk];
-    int64_t c[64][kChunk];
-    int32_t tokens[GA_MAX_WORKERS];
+    double p[THREADS / kChunk][kChunk];
+    int64_t c[THREADS / kChunk][kChunk];
+    int64_t n[THREADS / kChunk];
     double dot[kChunk];
 };
 
-template <int THREADS>
-__device__ __forceinline__ void sum_tokens(const LossArgs& a, const LoadParts& q, EndScratch& s) {
-    for (int w = threadIdx.x; w < a.W; w += THREADS) s.tokens[w] = 0;
-    __syncthreads();
-    for (int r = threadIdx.x; r < a.W * q.parts; r += THREADS) atomicAdd(&s.tokens[r / q.parts], q.tokens[r]);
-    __syncthreads();
-}
+// 1 / tokens; 0 without tokens.
+__device__ __forceinline__ double share_of(int64_t n) { return n > 0 ? 1.0 / (double)n : 0.0; }
 
-// 1 / tokens, of all workers or of worker w; 0 without tokens.
-__device__ __forceinline__ double share_of(const LossArgs& a, const EndScratch& s, int w) {
-    int64_t n = 0;
-    if (a.scope == GA_BALANCE_ALL) {
-        for (int i = 0; i < a.W; ++i) n += s.tokens[i];
-    } else {
-        n = s.tokens[w];
-    }
-    return n > 0 ? 1.0 / (double)n : 0.0;
-}
-
+// Ends the load of chunk `chunk` of the experts: the workers' counts and sums, and the slope; returns the chunk's part
+// of the balance loss in thread 0.  kChunk threads side by side take an expert each, THREADS / kChunk of them share its
+// partial rows.
 template <int THREADS>
-__device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& q, EndScratch& s, int chunk) {
+__device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& q, EndScratch<THREADS>& s, int chunk) {
     constexpr int SLICES = THREADS / kChunk;
     const int col = threadIdx.x & (kChunk - 1), slice = threadIdx.x / kChunk, e = chunk * kChunk + col;
     int at_once = 1;                                      // workers taken together
     while (at_once * 2 <= SLICES && at_once < a.W) at_once *= 2;
     const int per = SLICES / at_once, wl = slice / per, ps = slice % per;
     const bool all = a.scope == GA_BALANCE_ALL;
-    const double total = all ? share_of(a, s, 0) : 0.0;
     double P = 0.0, dot = 0.0;
-    int64_t F = 0;
+    int64_t F = 0, all_n = 0;
     for (int w0 = 0; w0 < a.W; w0 += at_once) {
         const int w = w0 + wl;
         double p = 0.0;
-        int64_t c = 0;
+        int64_t c = 0, n = 0;
         if (w < a.W && e < a.E) {
-#pragma unroll 4
+#pragma unroll 8
             for (int i = ps; i < q.parts; i += per) {
-                const int64_t at = ((int64_t)w * q.parts + i) * a.E + e;
+                const int64_t row = (int64_t)w * q.parts + i, at = row * a.E + e;
                 p += (double)q.probs[at];
                 c += q.counts[at];
+                n += q.tokens[row];
             }
         }
         __syncthreads();
         s.p[slice][col] = p;
         s.c[slice][col] = c;
+        if (col == 0) s.n[slice] = n;
         __syncthreads();
         if (ps != 0 || w >= a.W || e >= a.E) continue;
         for (int i = 1; i < per; ++i) {
             p += s.p[slice + i][col];
             c += s.c[slice + i][col];
+            n += s.n[slice + i];
         }
         a.load.probs[(int64_t)w * a.E + e] = (float)p;
         a.load.counts[(int64_t)w * a.E + e] = (int32_t)c;
         P += p;
         F += c;
+        all_n += n;
         if (!all) {
-            const double share = share_of(a, s, w), slope = (double)c * a.E / a.k * share * share / a.W;
+            const double share = share_of(n), slope = (double)c * a.E / a.k * share * share / a.W;
             a.load.slope[(int64_t)w * (a.E + 1) + e] = (float)slope;
             dot += slope * p;
         }
@@ -199,15 +210,17 @@ __device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& 
     __syncthreads();
     s.p[slice][col] = all ? P : dot;
     s.c[slice][col] = F;
+    if (col == 0) s.n[slice] = all_n;
     __syncthreads();
     if (slice == 0) {
         for (int i = 1; i < at_once; ++i) {
             P += s.p[i * per][col];
             dot += s.p[i * per][col];
             F += s.c[i * per][col];
+            all_n += s.n[i * per];
         }
         if (all) {
-            const double slope = (double)F * a.E / a.k * total * total;
+            const double share = share_of(all_n), slope = (double)F * a.E / a.k * share * share;
             if (e < a.E) a.load.slope[e] = (float)slope;
             dot = slope * P;
         }
@@ -216,29 +229,50 @@ __device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& 
     __syncthreads();
     if (threadIdx.x != 0) return 0.0;
     double sum = 0.0;
+#pragma unroll
     for (int i = 0; i < kChunk; ++i) sum += s.dot[i];
     return sum;
 }
 
-// What is not of a chunk: the workers' tokens, the z loss, and the slope's last column.
+// What is not of a chunk: the workers' tokens, the z loss, and the slope's last column.  A wavefront takes a worker.
 template <int THREADS>
-__device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, const EndScratch& s) {
+__device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, EndScratch<THREADS>& s) {
     const bool all = a.scope == GA_BALANCE_ALL;
-    for (int w = threadIdx.x; w < a.W; w += THREADS) {
-        a.load.tokens[w] = s.tokens[w];
-        if (!all) a.load.slope[(int64_t)w * (a.E + 1) + a.E] = (float)(2.0 * share_of(a, s, w) / a.W);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    double Z = 0.0;
+    int64_t all_n = 0;
+    for (int w = wave; w < a.W; w += THREADS / 64) {
+        double z = 0.0;
+        int32_t n = 0;
+#pragma unroll 4
+        for (int i = lane; i < q.parts; i += 64) {
+            z += q.squares[(int64_t)w * q.parts + i];
+            n += q.tokens[(int64_t)w * q.parts + i];
+        }
+        z = wave_sum_f64(z);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+        all_n += n;
+        const double share = share_of(n) / a.W;
+        Z += all ? z : z * share;
+        if (lane == 0) {
+            a.load.tokens[w] = n;
+            if (!all) a.load.slope[(int64_t)w * (a.E + 1) + a.E] = (float)(2.0 * share);
+        }
     }
-    if (threadIdx.x >= 64) return;
-    const double total = all ? share_of(a, s, 0) : 0.0;
-    double z = 0.0;
-    for (int r = threadIdx.x; r < a.W * q.parts; r += 64) {
-        const double share = all ? total : share_of(a, s, r / q.parts) / a.W;
-        if (share > 0.0) z += q.squares[r] * share;
+    __syncthreads();
+    if (lane == 0) {
+        s.p[wave][0] = Z;
+        s.c[wave][0] = all_n;
     }
-    z = wave_sum_f64(z);
+    __syncthreads();
     if (threadIdx.x != 0) return;
-    a.load.loss[1] = (float)z;
-    if (all) a.load.slope[a.E] = (float)(2.0 * total);
+    for (int i = 1; i < THREADS / 64; ++i) {
+        Z += s.p[i][0];
+        all_n += s.c[i][0];
+    }
+    a.load.loss[1] = (float)(all ? Z * share_of(all_n) : Z);
+    if (all) a.load.slope[a.E] = (float)(2.0 * share_of(all_n));
 }
 
 // Whether this workgroup is the last of n to get here; what the others stored before is then visible.  Each wavefront
@@ -259,26 +293,33 @@ __device__ __forceinline__ bool last_of(uint32_t* done, uint32_t n) {
 
 constexpr int kEndThreads = 1024;
 
+// A workgroup for each chunk, and one for the rest.
 __global__ __launch_bounds__(kEndThreads) void k_load_end(LossArgs a, LoadParts q) {
-    __shared__ EndScratch s;
-    sum_tokens<kEndThreads>(a, q, s);
+    __shared__ EndScratch<kEndThreads> s;
+    if (blockIdx.x + 1 == gridDim.x) {
+        end_rest<kEndThreads>(a, q, s);
+        return;
+    }
     const double dot = end_chunk<kEndThreads>(a, q, s, (int)blockIdx.x);
-    if (blockIdx.x == 0) end_rest<kEndThreads>(a, q, s);
     if (threadIdx.x == 0) q.dots[blockIdx.x] = dot;
-    if (!last_of(q.done, gridDim.x) || threadIdx.x != 0) return;
-    double loss = 0.0;
-    for (uint32_t i = 0; i < gridDim.x; ++i) loss += __hip_atomic_load(q.dots + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    a.load.loss[0] = (float)loss;
+    if (!last_of(q.done, gridDim.x - 1) || threadIdx.x >= 64) return;
+    double loss = threadIdx.x + 1 < gridDim.x
+                      ? __hip_atomic_load(q.dots + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    loss = wave_sum_f64(loss);
+    if (threadIdx.x == 0) a.load.loss[0] = (float)loss;
 }
+
+static_assert(GA_MAX_EXPERTS / kChunk <= 64, "a wavefront adds the chunks");
 
 // ---- forward -----------------------------------------------------------------
 
-template <int X, int L, int V, bool LOAD>
-__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, LoadParts q, int32_t normalize, int32_t one) {
+// LOAD 0: the routing alone; 1: partial loads too; 2: and the workgroup that ends last adds them (which takes registers).
+template <int X, int L, int V, int LOAD>
+__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, LoadParts q, int32_t normalize) {
     constexpr int TEAMS = kThreads / L, N = kVec<X>, J = V / N, EMAX = L * V;
     // while tokens are routed: the candidates of each team; then the wavefronts' sums; then what ends the load
     constexpr size_t LISTS = sizeof(uint64_t) * TEAMS * EMAX, COLS = sizeof(float) * kWaves * EMAX;
-    constexpr size_t MORE = LOAD ? (COLS > sizeof(EndScratch) ? COLS : sizeof(EndScratch)) : 0;
+    constexpr size_t ENDS = sizeof(EndScratch<kThreads>), MORE = LOAD ? (COLS > ENDS ? COLS : ENDS) : 0;
     __shared__ __align__(16) char pool[LISTS > MORE ? LISTS : MORE];
     __shared__ int32_t hist[LOAD ? EMAX : 1];
     __shared__ float slots[TEAMS][EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK];
@@ -335,21 +376,13 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
         uint64_t* list = reinterpret_cast<uint64_t*>(pool) + team * EMAX;
         int found = k;
         if (a.select) {
-            // k times the largest of the lanes' own maxima below the last one: at least k logits are not below it
+            // A bound that at least k logits reach: the k-th of the maxima of groups of logits, found one after the
+            // other.  Few groups are quick to go through, four times k of them or more leave few logits above the bound.
             float bound = INFINITY;
-            if (k <= L) {
-                float mine = l[0];
-#pragma unroll
-                for (int i = 1; i < V; ++i) mine = fmaxf(mine, l[i]);
-                for (int j = 0; j < k; ++j) bound = team_max<L>(mine < bound ? mine : -INFINITY);
-            } else {
-                for (int j = 0; j < k; ++j) {
-                    float mine = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) mine = fmaxf(mine, l[i] < bound ? l[i] : -INFINITY);
-                    bound = team_max<L>(mine);
-                }
-            }
+            if (4 * k <= L) bound = kth_of_groups<L, V, 1>(l, k);
+            else if (V >= 4 && 4 * k <= 2 * L) bound = kth_of_groups<L, V, 2>(l, k);
+            else if (V >= 8 && 4 * k <= 4 * L) bound = kth_of_groups<L, V, 4>(l, k);
+            else bound = kth_of_groups<L, V, V>(l, k);
             bound = fmaxf(bound, -3.402823466e38f);
             int count = 0;
 #pragma unroll
@@ -440,10 +473,10 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
             q.squares[row] = s;
             q.tokens[row] = n;
         }
-        if (!one) return;
+    }
+    if constexpr (LOAD == 2) {
         if (!last_of(q.done + 1, gridDim.x)) return;
-        EndScratch& end_scratch = *reinterpret_cast<EndScratch*>(pool);
-        sum_tokens<kThreads>(la, q, end_scratch);
+        EndScratch<kThreads>& end_scratch = *reinterpret_cast<EndScratch<kThreads>*>(pool);
         end_rest<kThreads>(la, q, end_scratch);
         double loss = 0.0;
         for (int c = 0; c * kChunk < E; ++c) loss += end_chunk<kThreads>(la, q, end_scratch, c);
@@ -584,8 +617,8 @@ hipError_t with_team(int E, F f) {
         GA_TEAM(8, 8);
     }
     GA_TEAM(16, 8);
-    GA_TEAM(16, 16);
-    GA_TEAM(32, 16);
+    GA_TEAM(32, 8);
+    GA_TEAM(64, 8);
     GA_TEAM(64, 16);
 #undef GA_TEAM
     return hipErrorInvalidValue;
@@ -609,19 +642,20 @@ hipError_t router_fwd(const Router& r, const RouteArgs& args, hipStream_t s) {
         constexpr int L = decltype(lanes)::value, V = decltype(each)::value, TEAMS = kThreads / L;
         if (!a.with_load) {
             a.per_worker = a.T;
-            q.parts = (int32_t)parts_of(a.T, TEAMS, 2048);
-            hipLaunchKernelGGL((k_route<X, L, V, false>), dim3((unsigned)q.parts), dim3(kThreads), 0, s, a, la, q, r.normalize,
-                               0);
+            q.parts = (int32_t)parts_of(a.T, TEAMS, 4096);
+            hipLaunchKernelGGL((k_route<X, L, V, 0>), dim3((unsigned)q.parts), dim3(kThreads), 0, s, a, la, q, r.normalize);
             return hipGetLastError();
         }
         q.parts = (int32_t)parts_of(a.per_worker, TEAMS, r.rows / r.W);
         const int64_t rows = (int64_t)r.W * q.parts;
-        const bool one = rows * r.E <= kOneLaunch;
-        hipLaunchKernelGGL((k_route<X, L, V, true>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, la, q, r.normalize,
-                           one ? 1 : 0);
+        if (rows * r.E <= kOneLaunch) {
+            hipLaunchKernelGGL((k_route<X, L, V, 2>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, la, q, r.normalize);
+            return hipGetLastError();
+        }
+        hipLaunchKernelGGL((k_route<X, L, V, 1>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, la, q, r.normalize);
         const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || one) return e;
-        hipLaunchKernelGGL(k_load_end, dim3((unsigned)((r.E + kChunk - 1) / kChunk)), dim3(kEndThreads), 0, s, la, q);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k_load_end, dim3((unsigned)((r.E + kChunk - 1) / kChunk) + 1), dim3(kEndThreads), 0, s, la, q);
         return hipGetLastError();
     });
 }
@@ -637,7 +671,7 @@ hipError_t router_bwd(const Router& r, const RouteArgs& args, hipStream_t s) {
             a.per_worker = a.T;
             workers = 1;
         }
-        const int64_t parts = parts_of(a.per_worker, TEAMS, 1024 / workers);
+        const int64_t parts = parts_of(a.per_worker, TEAMS, 2048 / workers);
         hipLaunchKernelGGL((k_route_bwd<X, L, V>), dim3((unsigned)(workers * parts)), dim3(kThreads), 0, s, a, la, r.normalize,
                            (int32_t)parts);
         return hipGetLastError();
