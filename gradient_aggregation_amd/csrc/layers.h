@@ -62,7 +62,7 @@ struct Router {
     uint32_t* d_done;      // [2] workgroups that have ended; 0 between calls
 };
 
-constexpr int kRouterRows = 1024;
+constexpr int kRouterRows = 256;
 
 struct RouteArgs {
     int64_t T, per_worker;    // tokens, tokens of a worker

@@ -10,7 +10,7 @@ namespace ga {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kLoadThreads = 1024;     // of a workgroup that leaves a partial load: few of them, so that few rows are added
 constexpr float kLog2e = 1.44269504f;
 
 // ---- teams of L lanes (a power of 2, aligned), all of whose lanes get the result ----
@@ -40,23 +40,33 @@ __device__ __forceinline__ float team_sum(float x) {
 }
 
 template <int L>
-__device__ __forceinline__ float team_max(float x) {
-    return __uint_as_float(team_reduce<L>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-    }));
+__device__ __forceinline__ uint32_t team_max(uint32_t x) {
+    return team_reduce<L>(x, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
-// Sum of the lower lanes' values.
 template <int L>
-__device__ __forceinline__ int team_before(int x) {
+__device__ __forceinline__ int team_sum(int x) {
+    return (int)team_reduce<L>((uint32_t)x, [](uint32_t a, uint32_t b) { return a + b; });
+}
+
+// Sum of the team's lanes up to this one: within a row of 16 lanes by shifts, over rows by broadcasts of the last lane.
+template <int L>
+__device__ __forceinline__ int team_scan(int x) {
     const int ln = threadIdx.x & (L - 1);
-    int s = x;
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-        const int y = __shfl_up(s, o, L);
-        if (ln >= o) s += y;
+    const auto from = [&](uint32_t y, int back) { return ln >= back ? (int)y : 0; };
+    if constexpr (L >= 2) x += from(lane_move<0x111>((uint32_t)x), 1);
+    if constexpr (L >= 4) x += from(lane_move<0x112>((uint32_t)x), 2);
+    if constexpr (L >= 8) x += from(lane_move<0x114>((uint32_t)x), 4);
+    if constexpr (L >= 16) x += from(lane_move<0x118>((uint32_t)x), 8);
+    if constexpr (L >= 32) {
+        const int y = __shfl(x, (threadIdx.x & 63 & ~31) + 15, 64);
+        if (ln & 16) x += y;
     }
-    return s - x;
+    if constexpr (L >= 64) {
+        const int y = __shfl(x, 31, 64);
+        if (ln & 32) x += y;
+    }
+    return x;
 }
 
 // What one lane of a wavefront wrote to LDS, another may now read: the hardware keeps a wavefront's accesses in order,
@@ -97,34 +107,40 @@ struct Lane {
     }
 };
 
-// A logit as a number whose order is its own (zeros of both signs alike), below it the index, the lowest on top.
-__device__ __forceinline__ uint64_t key_of(float v, int column) {
+// A logit as a whole number of the same order; zeros of both signs alike; a NaN, as the least (never selected), 0.
+// -infinity is kLeast.
+constexpr uint32_t kLeast = 0x007fffffu;
+
+__device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);
-    return (uint64_t)(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) << 32 | (uint32_t)~column;
+    const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return v == v ? key : 0u;
 }
 
-__device__ __forceinline__ float value_of(uint64_t key) {
-    const uint32_t u = (uint32_t)(key >> 32);
-    return __uint_as_float(u ^ ((int32_t)u < 0 ? 0x80000000u : 0xffffffffu));
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float(key ^ ((int32_t)key < 0 ? 0x80000000u : 0xffffffffu));
 }
 
-// Of the maxima of the team's L * GROUPS groups of logits (a lane's V are GROUPS of them), the k-th when equal ones count
-// once; -infinity where there are fewer.
+// Of the maxima of the team's L * GROUPS groups of keys (a lane's V are GROUPS of them), the k-th when equal ones count
+// once, the first one given; 0 where there are fewer.
 template <int L, int V, int GROUPS>
-__device__ __forceinline__ float kth_of_groups(const float (&l)[V], int k) {
+__device__ __forceinline__ uint32_t kth_of_groups(const uint32_t (&key)[V], uint32_t first, int k) {
     constexpr int EACH = V / GROUPS;
-    float top[GROUPS];
+    uint32_t top[GROUPS];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
-        top[g] = l[g * EACH];
+        top[g] = key[g * EACH];
 #pragma unroll
-        for (int i = 1; i < EACH; ++i) top[g] = fmaxf(top[g], l[g * EACH + i]);
+        for (int i = 1; i < EACH; ++i) top[g] = top[g] > key[g * EACH + i] ? top[g] : key[g * EACH + i];
     }
-    float bound = INFINITY;
-    for (int j = 0; j < k; ++j) {
-        float best = -INFINITY;
+    uint32_t bound = first;
+    for (int j = 1; j < k; ++j) {
+        uint32_t best = 0u;
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) best = fmaxf(best, top[g] < bound || j == 0 ? top[g] : -INFINITY);
+        for (int g = 0; g < GROUPS; ++g) {
+            const uint32_t x = top[g] < bound ? top[g] : 0u;
+            best = best > x ? best : x;
+        }
         bound = team_max<L>(best);
     }
     return bound;
@@ -314,12 +330,12 @@ static_assert(GA_MAX_EXPERTS / kChunk <= 64, "a wavefront adds the chunks");
 // ---- forward -----------------------------------------------------------------
 
 // LOAD 0: the routing alone; 1: partial loads too; 2: and the workgroup that ends last adds them (which takes registers).
-template <int X, int L, int V, int LOAD>
-__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, LoadParts q, int32_t normalize) {
-    constexpr int TEAMS = kThreads / L, N = kVec<X>, J = V / N, EMAX = L * V;
+template <int X, int L, int V, int LOAD, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, LoadParts q, int32_t normalize) {
+    constexpr int TEAMS = THREADS / L, N = kVec<X>, J = V / N, EMAX = L * V;
     // while tokens are routed: the candidates of each team; then the wavefronts' sums; then what ends the load
-    constexpr size_t LISTS = sizeof(uint64_t) * TEAMS * EMAX, COLS = sizeof(float) * kWaves * EMAX;
-    constexpr size_t ENDS = sizeof(EndScratch<kThreads>), MORE = LOAD ? (COLS > ENDS ? COLS : ENDS) : 0;
+    constexpr size_t LISTS = sizeof(uint64_t) * TEAMS * EMAX, COLS = sizeof(float) * (THREADS / 64) * EMAX;
+    constexpr size_t ENDS = sizeof(EndScratch<THREADS>), MORE = LOAD ? (COLS > ENDS ? COLS : ENDS) : 0;
     __shared__ __align__(16) char pool[LISTS > MORE ? LISTS : MORE];
     __shared__ int32_t hist[LOAD ? EMAX : 1];
     __shared__ float slots[TEAMS][EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK];
@@ -335,7 +351,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
     if constexpr (LOAD) {
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        for (int e = threadIdx.x; e < EMAX; e += kThreads) hist[e] = 0;
+        for (int e = threadIdx.x; e < EMAX; e += THREADS) hist[e] = 0;
         __syncthreads();
     }
     Raw<X, N> next[J];
@@ -349,19 +365,26 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
         float l[V], p[V];
         lane.widen(next, l, next_present);
         if (t + step < end) load(t + step);
-        float top = l[0], sum = 0.f;
-#pragma unroll
-        for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
-        top = team_max<L>(top);
-        const float from = top == -INFINITY ? 0.f : top;      // then all are -infinity (p = 0) or NaN
+        uint32_t key[V], most = 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = __builtin_amdgcn_exp2f((l[i] - from) * kLog2e);
+            key[i] = key_of(l[i]);
+            most = most > key[i] ? most : key[i];
+        }
+        most = team_max<L>(most);
+        // where all are -infinity or NaN, p is 0 or NaN
+        const float top = most > kLeast ? value_of(most) : 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = __builtin_amdgcn_exp2f((l[i] - top) * kLog2e);
             sum += p[i];
         }
         sum = team_sum<L>(sum);
+        // the hardware's reciprocal and logarithm, each within 1 ulp
         const bool absent = sum == 0.f;
-        const float inv = absent ? 0.f : 1.f / sum, lse = absent ? 0.f : top + logf(sum);
+        const float inv = absent ? 0.f : __builtin_amdgcn_rcpf(sum);
+        const float lse = absent ? 0.f : fmaf(__builtin_amdgcn_logf(sum), 0.693147181f, top);
         if constexpr (LOAD) {
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
@@ -378,20 +401,20 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
         if (a.select) {
             // A bound that at least k logits reach: the k-th of the maxima of groups of logits, found one after the
             // other.  Few groups are quick to go through, four times k of them or more leave few logits above the bound.
-            float bound = INFINITY;
-            if (4 * k <= L) bound = kth_of_groups<L, V, 1>(l, k);
-            else if (V >= 4 && 4 * k <= 2 * L) bound = kth_of_groups<L, V, 2>(l, k);
-            else if (V >= 8 && 4 * k <= 4 * L) bound = kth_of_groups<L, V, 4>(l, k);
-            else bound = kth_of_groups<L, V, V>(l, k);
-            bound = fmaxf(bound, -3.402823466e38f);
+            uint32_t bound;
+            if (4 * k <= L) bound = kth_of_groups<L, V, 1>(key, most, k);
+            else if (V >= 4 && 4 * k <= 2 * L) bound = kth_of_groups<L, V, 2>(key, most, k);
+            else if (V >= 8 && 4 * k <= 4 * L) bound = kth_of_groups<L, V, 4>(key, most, k);
+            else bound = kth_of_groups<L, V, V>(key, most, k);
+            bound = bound > kLeast ? bound : kLeast + 1u;
             int count = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) count += l[i] >= bound ? 1 : 0;
-            int at = team_before<L>(count);
-            found = __shfl(at + count, L - 1, L);
+            for (int i = 0; i < V; ++i) count += key[i] >= bound ? 1 : 0;
+            found = team_sum<L>(count);
+            int at = team_scan<L>(count) - count;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (l[i] >= bound) list[at++] = key_of(l[i], lane.column(i));
+                if (key[i] >= bound) list[at++] = (uint64_t)key[i] << 32 | (uint32_t)~lane.column(i);
         }
         wave_fence();
         float chosen = 0.f;
@@ -399,22 +422,24 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
             int rank = c, at = -1;
             float g = 0.f;
             if (a.select) {
-                const uint64_t key = list[c];
+                const uint64_t mine = list[c];
                 rank = 0;
-                for (int j = 0; j < found; ++j) rank += list[j] > key ? 1 : 0;
+#pragma unroll 4
+                for (int j = 0; j < found; ++j) rank += list[j] > mine ? 1 : 0;
                 if (rank >= k) continue;
-                at = (int)~(uint32_t)key;
-                g = __builtin_amdgcn_exp2f((value_of(key) - from) * kLog2e);
+                at = (int)~(uint32_t)mine;
+                g = __builtin_amdgcn_exp2f((value_of((uint32_t)(mine >> 32)) - top) * kLog2e);
                 experts[rank] = at;
             } else {
                 at = experts[c];
                 if (at < 0 || at >= E) at = -1;
                 if (at >= 0 && !absent) {
                     const float x = load_one<X>(reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx + at * kSize<X>));
-                    g = __builtin_amdgcn_exp2f((x - from) * kLog2e);
+                    g = __builtin_amdgcn_exp2f((x - top) * kLog2e);
                 }
             }
             slots[team][rank] = g;
+            chosen += g;
             if (LOAD && at >= 0 && !absent) atomicAdd(&hist[at], 1);
         }
         if (a.select) {
@@ -426,9 +451,9 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
         wave_fence();
         if (gates) {
             float by = inv;
-            if (normalize && !absent) {
-                for (int j = 0; j < k; ++j) chosen += slots[team][j];
-                by = sum != sum ? sum : chosen == 0.f ? 0.f : 1.f / chosen;
+            if (normalize) {
+                chosen = team_sum<L>(chosen);
+                by = sum != sum ? sum : chosen == 0.f ? 0.f : __builtin_amdgcn_rcpf(chosen);
             }
             for (int j = ln; j < k; j += L) gates[j] = absent ? 0.f : slots[team][j] * by;
         }
@@ -437,8 +462,8 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
     if constexpr (LOAD) {
         // the wavefront's teams, then the wavefronts, in order
         float(*cols)[EMAX] = reinterpret_cast<float(*)[EMAX]>(pool);
-        __shared__ double sq[kWaves];
-        __shared__ int32_t tok[kWaves];
+        __shared__ double sq[(THREADS / 64)];
+        __shared__ int32_t tok[(THREADS / 64)];
         const int wave = threadIdx.x >> 6;
         __syncthreads();
 #pragma unroll
@@ -456,17 +481,17 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
         }
         __syncthreads();
         const int64_t row = blockIdx.x;
-        for (int e = threadIdx.x; e < E; e += kThreads) {
+        for (int e = threadIdx.x; e < E; e += THREADS) {
             float s = cols[0][e];
 #pragma unroll
-            for (int j = 1; j < kWaves; ++j) s += cols[j][e];
+            for (int j = 1; j < (THREADS / 64); ++j) s += cols[j][e];
             q.probs[row * E + e] = s;
             q.counts[row * E + e] = hist[e];
         }
         if (threadIdx.x == 0) {
             double s = sq[0];
             int n = tok[0];
-            for (int j = 1; j < kWaves; ++j) {
+            for (int j = 1; j < (THREADS / 64); ++j) {
                 s += sq[j];
                 n += tok[j];
             }
@@ -476,17 +501,17 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, LossArgs la, Lo
     }
     if constexpr (LOAD == 2) {
         if (!last_of(q.done + 1, gridDim.x)) return;
-        EndScratch<kThreads>& end_scratch = *reinterpret_cast<EndScratch<kThreads>*>(pool);
-        end_rest<kThreads>(la, q, end_scratch);
+        EndScratch<THREADS>& end_scratch = *reinterpret_cast<EndScratch<THREADS>*>(pool);
+        end_rest<THREADS>(la, q, end_scratch);
         double loss = 0.0;
-        for (int c = 0; c * kChunk < E; ++c) loss += end_chunk<kThreads>(la, q, end_scratch, c);
+        for (int c = 0; c * kChunk < E; ++c) loss += end_chunk<THREADS>(la, q, end_scratch, c);
         if (threadIdx.x == 0) la.load.loss[0] = (float)loss;
     }
 }
 
 // ---- backward ----------------------------------------------------------------
 
-template <int X, int L, int V>
+template <int X, int L, int V, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteArgs a, LossArgs la, int32_t normalize, int32_t parts) {
     constexpr int TEAMS = kThreads / L, N = kVec<X>, J = V / N, EMAX = L * V;
     constexpr int SLOTS = (EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK) > L ? (EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK) / L : 1;
@@ -525,14 +550,10 @@ __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteArgs a, LossArgs la
         float g[SLOTS], inner = 0.f;
         if (a.dgates) {
             if (lse == 0.f) {       // perhaps of a token without an expert
-                float top = l[0];
-                bool nan = l[0] != l[0];
+                bool some = false;
 #pragma unroll
-                for (int i = 1; i < V; ++i) {
-                    top = fmaxf(top, l[i]);
-                    nan |= l[i] != l[i];
-                }
-                present = team_max<L>(nan ? INFINITY : top) > -INFINITY;
+                for (int i = 0; i < V; ++i) some |= l[i] != -INFINITY;
+                present = team_max<L>(some ? 1u : 0u) != 0u;
             }
 #pragma unroll
             for (int s = 0; s < SLOTS; ++s) {
@@ -556,12 +577,34 @@ __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteArgs a, LossArgs la
 #pragma unroll
                 for (int s = 0; s < SLOTS; ++s) g[s] = gate[s] * (g[s] - inner);
             }
-            // one slot after the other, so that the same expert twice adds up in their order
+            // each slot leaves its number with its expert: where another's stands then, an expert was given twice
+            bool twice = false;
 #pragma unroll
-            for (int s = 0; s < SLOTS; ++s) {
-                const int many = k - s * L < L ? k - s * L : L;
-                for (int j = 0; j < many; ++j)
-                    if (ln == j && at[s] >= 0) atomicAdd(&extra[team][at[s]], g[s]);
+            for (int s = 0; s < SLOTS; ++s)
+                if (at[s] >= 0) extra[team][at[s]] = __int_as_float(s * L + ln);
+            wave_fence();
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s)
+                if (at[s] >= 0) twice |= __float_as_int(extra[team][at[s]]) != s * L + ln;
+            wave_fence();
+            if (__ballot(twice) == 0ull) {
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s)
+                    if (at[s] >= 0) extra[team][at[s]] = g[s];
+            } else {
+                // one slot after the other, so that they add up in their order
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s)
+                    if (at[s] >= 0) extra[team][at[s]] = 0.f;
+                wave_fence();
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s) {
+                    const int many = k - s * L < L ? k - s * L : L;
+                    for (int j = 0; j < many; ++j) {
+                        if (ln == j && at[s] >= 0) extra[team][at[s]] += g[s];
+                        wave_fence();
+                    }
+                }
             }
             wave_fence();
         }
@@ -592,7 +635,7 @@ __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteArgs a, LossArgs la
                 const int i = j * N + e;
                 d[e] = present ? fmaf(l[i], h[i] + shift, direct[i]) : 0.f;
             }
-            store_part<X>(d, out, (j * L + ln) * N, E);
+            store_part<X, STREAM>(d, out, (j * L + ln) * N, E);
         }
     }
 }
@@ -617,8 +660,8 @@ hipError_t with_team(int E, F f) {
         GA_TEAM(8, 8);
     }
     GA_TEAM(16, 8);
-    GA_TEAM(32, 8);
-    GA_TEAM(64, 8);
+    GA_TEAM(16, 16);
+    GA_TEAM(32, 16);
     GA_TEAM(64, 16);
 #undef GA_TEAM
     return hipErrorInvalidValue;
@@ -639,20 +682,24 @@ hipError_t router_fwd(const Router& r, const RouteArgs& args, hipStream_t s) {
     const LossArgs la = {a.load, r.E, r.k, r.W, r.scope};
     LoadParts q = {r.d_probs, r.d_counts, r.d_squares, r.d_tokens, r.d_dots, r.d_done, 1};
     return with_team<X>(r.E, [&](auto lanes, auto each) {
-        constexpr int L = decltype(lanes)::value, V = decltype(each)::value, TEAMS = kThreads / L;
+        constexpr int L = decltype(lanes)::value, V = decltype(each)::value;
         if (!a.with_load) {
             a.per_worker = a.T;
-            q.parts = (int32_t)parts_of(a.T, TEAMS, 4096);
-            hipLaunchKernelGGL((k_route<X, L, V, 0>), dim3((unsigned)q.parts), dim3(kThreads), 0, s, a, la, q, r.normalize);
+            q.parts = (int32_t)parts_of(a.T, kThreads / L, 4096);
+            hipLaunchKernelGGL((k_route<X, L, V, 0, kThreads>), dim3((unsigned)q.parts), dim3(kThreads), 0, s, a, la, q,
+                               r.normalize);
             return hipGetLastError();
         }
-        q.parts = (int32_t)parts_of(a.per_worker, TEAMS, r.rows / r.W);
+        q.parts = (int32_t)parts_of(a.per_worker, kThreads / L, r.rows / r.W);
+        if (r.W * q.parts * (int64_t)r.E <= kOneLaunch) {
+            hipLaunchKernelGGL((k_route<X, L, V, 2, kThreads>), dim3((unsigned)(r.W * q.parts)), dim3(kThreads), 0, s, a, la,
+                               q, r.normalize);
+            return hipGetLastError();
+        }
+        q.parts = (int32_t)parts_of(a.per_worker, kLoadThreads / L, r.rows / r.W);
         const int64_t rows = (int64_t)r.W * q.parts;
-        if (rows * r.E <= kOneLaunch) {
-            hipLaunchKernelGGL((k_route<X, L, V, 2>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, la, q, r.normalize);
-            return hipGetLastError();
-        }
-        hipLaunchKernelGGL((k_route<X, L, V, 1>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, la, q, r.normalize);
+        hipLaunchKernelGGL((k_route<X, L, V, 1, kLoadThreads>), dim3((unsigned)rows), dim3(kLoadThreads), 0, s, a, la, q,
+                           r.normalize);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k_load_end, dim3((unsigned)((r.E + kChunk - 1) / kChunk) + 1), dim3(kEndThreads), 0, s, la, q);
@@ -672,8 +719,15 @@ hipError_t router_bwd(const Router& r, const RouteArgs& args, hipStream_t s) {
             workers = 1;
         }
         const int64_t parts = parts_of(a.per_worker, TEAMS, 2048 / workers);
-        hipLaunchKernelGGL((k_route_bwd<X, L, V>), dim3((unsigned)(workers * parts)), dim3(kThreads), 0, s, a, la, r.normalize,
-                           (int32_t)parts);
+        // whole cache lines pass the caches by
+        const int64_t row = (int64_t)r.E * kSize<X>;
+        const bool stream = row % 128 == 0 && a.ldd % 128 == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 127) == 0;
+        if (stream)
+            hipLaunchKernelGGL((k_route_bwd<X, L, V, true>), dim3((unsigned)(workers * parts)), dim3(kThreads), 0, s, a, la,
+                               r.normalize, (int32_t)parts);
+        else
+            hipLaunchKernelGGL((k_route_bwd<X, L, V, false>), dim3((unsigned)(workers * parts)), dim3(kThreads), 0, s, a, la,
+                               r.normalize, (int32_t)parts);
         return hipGetLastError();
     });
 }
