@@ -260,7 +260,6 @@ __device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, 
     for (int w = wave; w < a.W; w += THREADS / 64) {
         double z = 0.0;
         int32_t n = 0;
-#pragma unroll 4
         for (int i = lane; i < q.parts; i += 64) {
             z += q.squares[(int64_t)w * q.parts + i];
             n += q.tokens[(int64_t)w * q.parts + i];
@@ -278,14 +277,14 @@ __device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, 
     }
     __syncthreads();
     if (lane == 0) {
-        s.p[wave][0] = Z;
-        s.c[wave][0] = all_n;
+        s.dot[wave] = Z;
+        s.n[wave] = all_n;
     }
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int i = 1; i < THREADS / 64; ++i) {
-        Z += s.p[i][0];
-        all_n += s.c[i][0];
+        Z += s.dot[i];
+        all_n += s.n[i];
     }
     a.load.loss[1] = (float)(all ? Z * share_of(all_n) : Z);
     if (all) a.load.slope[a.E] = (float)(2.0 * share_of(all_n));
@@ -311,12 +310,17 @@ constexpr int kEndThreads = 1024;
 
 // A workgroup for each chunk, and one for the rest.
 __global__ __launch_bounds__(kEndThreads) void k_load_end(LossArgs a, LoadParts q) {
+    static_assert(kEndThreads / 64 <= kChunk, "a place for each wavefront");
     __shared__ EndScratch<kEndThreads> s;
     if (blockIdx.x + 1 == gridDim.x) {
-        end_rest<kEndThreads>(a, q, s);
+        end_rest(a, q, s);
         return;
     }
-    const double dot = end_chunk<kEndThreads>(a, q, s, (int)blockIdx.x);
+    const double dot = end_chunk(a, q, s, (int)blockIdx.x);
+    if (gridDim.x == 2) {
+        if (threadIdx.x == 0) a.load.loss[0] = (float)dot;
+        return;
+    }
     if (threadIdx.x == 0) q.dots[blockIdx.x] = dot;
     if (!last_of(q.done, gridDim.x - 1) || threadIdx.x >= 64) return;
     double loss = threadIdx.x + 1 < gridDim.x
@@ -354,17 +358,20 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
         for (int e = threadIdx.x; e < EMAX; e += THREADS) hist[e] = 0;
         __syncthreads();
     }
+    // the next row is on its way, unless the registers are taken by 16 binary32 logits and sums to a lane
+    constexpr bool AHEAD = !(LOAD == 1 && X == kF32 && V == 16);
     Raw<X, N> next[J];
     bool next_present = false;
     auto load = [&](int64_t t) {
         next_present = !a.mask || a.mask[t];
         lane.load(next, reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx));
     };
-    if (t < end) load(t);
+    if (AHEAD && t < end) load(t);
     for (; t < end; t += step) {
         float l[V], p[V];
+        if (!AHEAD) load(t);
         lane.widen(next, l, next_present);
-        if (t + step < end) load(t + step);
+        if (AHEAD && t + step < end) load(t + step);
         uint32_t key[V], most = 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -501,10 +508,10 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
     }
     if constexpr (LOAD == 2) {
         if (!last_of(q.done + 1, gridDim.x)) return;
-        EndScratch<THREADS>& end_scratch = *reinterpret_cast<EndScratch<THREADS>*>(pool);
-        end_rest<THREADS>(la, q, end_scratch);
+        auto& end_scratch = *reinterpret_cast<EndScratch<THREADS>*>(pool);
+        end_rest(la, q, end_scratch);
         double loss = 0.0;
-        for (int c = 0; c * kChunk < E; ++c) loss += end_chunk<THREADS>(la, q, end_scratch, c);
+        for (int c = 0; c * kChunk < E; ++c) loss += end_chunk(la, q, end_scratch, c);
         if (threadIdx.x == 0) la.load.loss[0] = (float)loss;
     }
 }
@@ -642,8 +649,10 @@ __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteArgs a, LossArgs la
 
 // ---- on the host -------------------------------------------------------------
 
-// Calls f with the lanes of a team and the elements of a lane.
-template <int X, typename F>
+// Calls f with the lanes of a team and the elements of a lane.  129 to 256 experts: 16 lanes forward, where a token's steps
+// are what it costs (131072 x 256 binary32, 8 of them: 52 us, with 32 lanes of 8 elements 64), 32 lanes backward, whose
+// registers then leave room for more wavefronts (bf16: 31 us, 41).
+template <int X, bool BACKWARD, typename F>
 hipError_t with_team(int E, F f) {
 #define GA_TEAM(L, V) \
     if (E <= L * V) return f(std::integral_constant<int, L>{}, std::integral_constant<int, V>{})
@@ -660,8 +669,13 @@ hipError_t with_team(int E, F f) {
         GA_TEAM(8, 8);
     }
     GA_TEAM(16, 8);
-    GA_TEAM(16, 16);
-    GA_TEAM(32, 16);
+    if constexpr (BACKWARD) {
+        GA_TEAM(32, 8);
+        GA_TEAM(64, 8);
+    } else {
+        GA_TEAM(16, 16);
+        GA_TEAM(32, 16);
+    }
     GA_TEAM(64, 16);
 #undef GA_TEAM
     return hipErrorInvalidValue;
@@ -681,7 +695,7 @@ hipError_t router_fwd(const Router& r, const RouteArgs& args, hipStream_t s) {
     RouteArgs a = args;
     const LossArgs la = {a.load, r.E, r.k, r.W, r.scope};
     LoadParts q = {r.d_probs, r.d_counts, r.d_squares, r.d_tokens, r.d_dots, r.d_done, 1};
-    return with_team<X>(r.E, [&](auto lanes, auto each) {
+    return with_team<X, false>(r.E, [&](auto lanes, auto each) {
         constexpr int L = decltype(lanes)::value, V = decltype(each)::value;
         if (!a.with_load) {
             a.per_worker = a.T;
@@ -711,14 +725,15 @@ template <int X>
 hipError_t router_bwd(const Router& r, const RouteArgs& args, hipStream_t s) {
     RouteArgs a = args;
     const LossArgs la = {a.load, r.E, r.k, r.W, r.scope};
-    return with_team<X>(r.E, [&](auto lanes, auto each) {
+    return with_team<X, true>(r.E, [&](auto lanes, auto each) {
         constexpr int L = decltype(lanes)::value, V = decltype(each)::value, TEAMS = kThreads / L;
         int64_t workers = r.W;
         if (r.scope == GA_BALANCE_ALL) {
             a.per_worker = a.T;
             workers = 1;
         }
-        const int64_t parts = parts_of(a.per_worker, TEAMS, 2048 / workers);
+        // as many workgroups as the chip holds at once
+        const int64_t parts = parts_of(a.per_worker, TEAMS, (V <= 8 ? 1536 : 1024) / workers);
         // whole cache lines pass the caches by
         const int64_t row = (int64_t)r.E * kSize<X>;
         const bool stream = row % 128 == 0 && a.ldd % 128 == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 127) == 0;
