@@ -403,7 +403,11 @@ inline void lay_wide(GnShape& h, int N, int T, int64_t samples) {
     int64_t parts = ceil_div(512, samples * h.slabs);
     const int64_t most = ceil_div(h.S, kAhead * (int64_t)h.R), least = ceil_div(h.S, 256 * (int64_t)h.R);
     if (parts > most) parts = most;
-    if (parts < least) parts = least;    // a thread adds up at most some 256 rows, whose roundings add up too
+    // a thread adds up at most some 256 rows, whose roundings add up too, unless so many groups leave no room to (images of
+    // 17 GB and more)
+    if (parts < least) parts = least;
+    const int64_t room = kGnRecords / ((int64_t)h.pieces * h.G);
+    if (parts > room) parts = room;
     h.parts = (int)parts;
     const int64_t chunk = kAhead * (int64_t)h.R, all = h.S / chunk;
     h.chunks = (int)(all / parts);

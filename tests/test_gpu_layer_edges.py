@@ -160,3 +160,60 @@ def test_two_handles_on_two_streams(ga):
     torch.cuda.synchronize()
     for (_, outs), w in zip(jobs, want):
         assert all(torch.equal(p, q) for p, q in zip(outs, w))
+
+
+@pytest.mark.parametrize("C,G,S", [(65536, 65536, 1 << 18), (32768, 16384, 9 << 16)])
+def test_long_images_of_many_groups(ga, C, G, S):
+    """More partial sums than the workspace holds, were a thread to add 256 rows at most: 34 GB, 64 rows repeated, in place."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    rows = torch.randn(64, C, generator=gen, device="cuda").bfloat16()
+    x = torch.empty(1, S, C, dtype=torch.bfloat16, device="cuda")
+    x.view(S // 64, 64, C).copy_(rows)
+    gn = ga.GroupNorm(C, G, torch.bfloat16, activation="relu")
+    mean, rstd = torch.full((2, 1, G), math.nan, device="cuda")
+    want = rows.double().reshape(64, G, C // G)
+    m = want.mean((0, 2))
+    d = want - m[:, None]
+    r = (d.square().mean((0, 2)) + 1e-5) ** -0.5
+    # a thread adds S / (16 * 32) rows or fewer; the roundings of so many equal terms add up
+    chain = S // 512 + 512
+    dev = d.abs().mean((0, 2)) + d.square().mean((0, 2)).sqrt()
+    gn.forward(x, None, None, x, mean, rstd)
+    assert bool(((mean[0].double() - m).abs() <= 2.0 ** -24 * (chain * dev + 2 * m.abs())).all())
+    assert bool(((rstd[0].double() / r - 1).abs() <= 2.0 ** -24 * (chain + 16)).all())
+    y = ((want - mean[0].double()[:, None]) * rstd[0].double()[:, None]).clamp_min(0).reshape(64, C)
+    for s in range(0, S, S // 8):
+        got = x[0, s:s + 64].double()
+        assert bool(((got - y).abs() <= (2.0 ** -8 + 2.0 ** -20) * y + 2.0 ** -20).all())
+    del x
+    # the gradient: every 64 rows alike again
+    x = torch.empty(1, S, C, dtype=torch.bfloat16, device="cuda")
+    x.view(S // 64, 64, C).copy_(rows)
+    dy = torch.empty_like(x)
+    grad = torch.randn(64, C, generator=gen, device="cuda").bfloat16()
+    dy.view(S // 64, 64, C).copy_(grad)
+    dg, db = torch.empty(2, 1, C, device="cuda")
+    xh = (want - mean[0].double()[:, None]) * rstd[0].double()[:, None]
+    h = torch.where(xh > 0, grad.double().reshape(64, G, C // G), torch.zeros_like(xh))
+    gn.backward(dy, x, None, None, mean, rstd, dy, dg, db)
+    part = (64, G, C // G)
+    for got, term in ((db, h), (dg, h * xh)):
+        want_sum = term.sum(0).reshape(C) * (S // 64)
+        size = term.abs().sum(0).reshape(C) * (S // 64)
+        assert bool(((got[0].double() - want_sum).abs() <= 2.0 ** -24 * (chain + 16) * size).all())
+    R = rstd[0].double()[:, None]
+    dx = R * (h - h.mean((0, 2))[:, None] - xh * (h * xh).mean((0, 2))[:, None])
+    err = 2.0 ** -24 * (chain + 16) * R * (h.abs().mean((0, 2))[:, None] + xh.abs() * (h * xh).abs().mean((0, 2))[:, None] + h.abs())
+    for s in range(0, S, S // 8):
+        got = dy[0, s:s + 64].double().reshape(part)
+        assert bool(((got - dx).abs() <= err + 2.0 ** -8 * (dx.abs() + err)).all())
+
+
+@pytest.mark.parametrize("x", ["fp32", "bf16"])
+def test_widest_slabs(ga, x):
+    """Groups that fill a workgroup's rows: the most shared memory that either pass takes."""
+    for N, S, C, G in ((3, 3, 4096, 1), (2, 8, 4096, 1), (2, 1, 4096, 2), (2, 4, 2048, 1), (3, 5, 8192, 2), (2, 600, 2048, 1)):
+        a, dy, gamma, beta = inputs(N, S, C, x, "fp32", "plain", S)
+        gnt.check_forward(ga, a, gamma, beta, G, "silu")
+        gnt.check_backward(ga, dy, a, gamma, beta, G, "silu", N)
+        gnt.check_backward(ga, dy, a, gamma, beta, G, "silu", 1)
