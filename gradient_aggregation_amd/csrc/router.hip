@@ -424,6 +424,19 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
                 if (key[i] >= bound) list[at++] = (uint64_t)key[i] << 32 | (uint32_t)~lane.column(i);
         }
         wave_fence();
+        // given experts may all lie far below the largest logit: gates that sum to 1 refer to the largest of theirs
+        float about = top;
+        if (!a.select && normalize) {
+            uint32_t best = 0u;
+            for (int c = ln; c < k; c += L) {
+                const int at = experts[c];
+                if (at < 0 || at >= E || absent) continue;
+                const uint32_t x = key_of(load_one<X>(reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx + at * kSize<X>)));
+                best = best > x ? best : x;
+            }
+            best = team_max<L>(best);
+            about = best > kLeast ? value_of(best) : 0.f;
+        }
         float chosen = 0.f;
         for (int c = ln; c < found; c += L) {
             int rank = c, at = -1;
@@ -442,7 +455,7 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
                 if (at < 0 || at >= E) at = -1;
                 if (at >= 0 && !absent) {
                     const float x = load_one<X>(reinterpret_cast<uint64_t>(a.x) + (uint64_t)(t * a.ldx + at * kSize<X>));
-                    g = __builtin_amdgcn_exp2f((x - top) * kLog2e);
+                    g = __builtin_amdgcn_exp2f((x - about) * kLog2e);
                 }
             }
             slots[team][rank] = g;

@@ -213,6 +213,26 @@ def test_given_experts(ga, shape, x):
         check_backward(ga, l, router, r, load, o, dgates)
 
 
+@pytest.mark.parametrize("x", ["fp32", "bf16"])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("below", [100.0, 400.0, 3e4])
+def test_given_experts_far_below_the_largest(ga, below, norm, x):
+    """Gates that sum to 1 come from the given experts' logits, however small their probabilities are."""
+    for T, E, k in ((70, 8, 2), (300, 60, 4), (50, 512, 32)):
+        l = logits(T, E, x, 3)
+        half = E // 2
+        l[:, :half] -= below
+        gen = torch.Generator(device="cuda").manual_seed(E)
+        given = torch.argsort(torch.rand(T, half, generator=gen, device="cuda"), dim=1)[:, :k].int()
+        l[3, given[3, 0].long()] = -INF             # one of a token's experts, and all of another's
+        l[5, given[5].long()] = -INF
+        given[7, 1] = -1
+        router, r, load, o = check_forward(ga, l, k, W=1, norm=norm, given=given)
+        if norm:
+            sums = r.gates.sum(1)
+            assert bool(((sums - 1).abs() <= (k + 4) * 2 * U)[torch.arange(T, device="cuda") != 5].all()) and float(sums[5]) == 0
+
+
 @pytest.mark.parametrize("x", ["fp32", "fp16", "bf16"])
 @pytest.mark.parametrize("E,k", [(4, 4), (8, 3), (40, 10), (64, 6), (256, 8), (300, 16), (1024, 32)])
 def test_ties_go_to_the_lowest_index(ga, E, k, x):
