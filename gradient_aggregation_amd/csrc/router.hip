@@ -157,31 +157,31 @@ struct LoadParts {
     int32_t parts;
 };
 
-constexpr int kChunk = 16;                                // experts of a chunk
-
 struct LossArgs {
     ga_load load;
     int32_t E, k, W, scope;
 };
 
-template <int THREADS>
+// CHUNK: experts of a chunk.
+template <int THREADS, int CHUNK>
 struct EndScratch {
-    double p[THREADS / kChunk][kChunk];
-    int64_t c[THREADS / kChunk][kChunk];
-    int64_t n[THREADS / kChunk];
-    double dot[kChunk];
+    double p[THREADS / CHUNK][CHUNK];
+    int64_t c[THREADS / CHUNK][CHUNK];
+    int64_t n[THREADS / CHUNK > THREADS / 64 ? THREADS / CHUNK : THREADS / 64];
+    double z[THREADS / 64];
 };
 
 // 1 / tokens; 0 without tokens.
 __device__ __forceinline__ double share_of(int64_t n) { return n > 0 ? 1.0 / (double)n : 0.0; }
 
 // Ends the load of chunk `chunk` of the experts: the workers' counts and sums, and the slope; returns the chunk's part
-// of the balance loss in thread 0.  kChunk threads side by side take an expert each, THREADS / kChunk of them share its
+// of the balance loss in thread 0.  CHUNK threads side by side take an expert each, THREADS / CHUNK of them share its
 // partial rows.
-template <int THREADS>
-__device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& q, EndScratch<THREADS>& s, int chunk) {
-    constexpr int SLICES = THREADS / kChunk;
-    const int col = threadIdx.x & (kChunk - 1), slice = threadIdx.x / kChunk, e = chunk * kChunk + col;
+template <int THREADS, int CHUNK>
+__device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& q, EndScratch<THREADS, CHUNK>& s, int chunk) {
+    constexpr int SLICES = THREADS / CHUNK, WAVE = 64 / CHUNK;
+    static_assert(CHUNK <= 64, "a wavefront adds the chunk's parts of the loss");
+    const int col = threadIdx.x & (CHUNK - 1), slice = threadIdx.x / CHUNK, e = chunk * CHUNK + col;
     int at_once = 1;                                      // workers taken together
     while (at_once * 2 <= SLICES && at_once < a.W) at_once *= 2;
     const int per = SLICES / at_once, wl = slice / per, ps = slice % per;
@@ -201,13 +201,22 @@ __device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& 
                 n += q.tokens[row];
             }
         }
+        // the slices of a wavefront, then the others
+#pragma unroll
+        for (int o = 1; o < WAVE; o <<= 1) {
+            if (o >= per) break;
+            p += __shfl_xor(p, o * CHUNK, 64);
+            c += __shfl_xor(c, o * CHUNK, 64);
+            n += __shfl_xor(n, o * CHUNK, 64);
+        }
         __syncthreads();
         s.p[slice][col] = p;
         s.c[slice][col] = c;
         if (col == 0) s.n[slice] = n;
         __syncthreads();
         if (ps != 0 || w >= a.W || e >= a.E) continue;
-        for (int i = 1; i < per; ++i) {
+#pragma unroll 4
+        for (int i = WAVE; i < per; i += WAVE) {
             p += s.p[slice + i][col];
             c += s.c[slice + i][col];
             n += s.n[slice + i];
@@ -229,6 +238,7 @@ __device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& 
     if (col == 0) s.n[slice] = all_n;
     __syncthreads();
     if (slice == 0) {
+#pragma unroll 4
         for (int i = 1; i < at_once; ++i) {
             P += s.p[i * per][col];
             dot += s.p[i * per][col];
@@ -240,19 +250,13 @@ __device__ __forceinline__ double end_chunk(const LossArgs& a, const LoadParts& 
             if (e < a.E) a.load.slope[e] = (float)slope;
             dot = slope * P;
         }
-        s.dot[col] = e < a.E ? dot : 0.0;
     }
-    __syncthreads();
-    if (threadIdx.x != 0) return 0.0;
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) sum += s.dot[i];
-    return sum;
+    return threadIdx.x < 64 ? wave_sum_f64(slice == 0 && e < a.E ? dot : 0.0) : 0.0;
 }
 
 // What is not of a chunk: the workers' tokens, the z loss, and the slope's last column.  A wavefront takes a worker.
-template <int THREADS>
-__device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, EndScratch<THREADS>& s) {
+template <int THREADS, int CHUNK>
+__device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, EndScratch<THREADS, CHUNK>& s) {
     const bool all = a.scope == GA_BALANCE_ALL;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     double Z = 0.0;
@@ -277,13 +281,13 @@ __device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, 
     }
     __syncthreads();
     if (lane == 0) {
-        s.dot[wave] = Z;
+        s.z[wave] = Z;
         s.n[wave] = all_n;
     }
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int i = 1; i < THREADS / 64; ++i) {
-        Z += s.dot[i];
+        Z += s.z[i];
         all_n += s.n[i];
     }
     a.load.loss[1] = (float)(all ? Z * share_of(all_n) : Z);
@@ -309,9 +313,9 @@ __device__ __forceinline__ bool last_of(uint32_t* done, uint32_t n) {
 constexpr int kEndThreads = 1024;
 
 // A workgroup for each chunk, and one for the rest.
+template <int CHUNK>
 __global__ __launch_bounds__(kEndThreads) void k_load_end(LossArgs a, LoadParts q) {
-    static_assert(kEndThreads / 64 <= kChunk, "a place for each wavefront");
-    __shared__ EndScratch<kEndThreads> s;
+    __shared__ EndScratch<kEndThreads, CHUNK> s;
     if (blockIdx.x + 1 == gridDim.x) {
         end_rest(a, q, s);
         return;
@@ -321,15 +325,25 @@ __global__ __launch_bounds__(kEndThreads) void k_load_end(LossArgs a, LoadParts 
         if (threadIdx.x == 0) a.load.loss[0] = (float)dot;
         return;
     }
-    if (threadIdx.x == 0) q.dots[blockIdx.x] = dot;
-    if (!last_of(q.done, gridDim.x - 1) || threadIdx.x >= 64) return;
+    if (threadIdx.x >= 64) return;
+    // The parts of the loss are all that passes between workgroups: they are stored past the caches, and have arrived
+    // before the count that says so, with no cache written back.
+    uint32_t last = 0;
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(q.dots + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last = __hip_atomic_fetch_add(q.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 2 == gridDim.x ? 1u : 0u;
+    }
+    if (__builtin_amdgcn_readfirstlane(last) == 0u) return;
+    asm volatile("" ::: "memory");
     double loss = threadIdx.x + 1 < gridDim.x
                       ? __hip_atomic_load(q.dots + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    if (threadIdx.x == 0) __hip_atomic_store(q.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     loss = wave_sum_f64(loss);
     if (threadIdx.x == 0) a.load.loss[0] = (float)loss;
 }
 
-static_assert(GA_MAX_EXPERTS / kChunk <= 64, "a wavefront adds the chunks");
+static_assert(GA_MAX_EXPERTS / 16 <= 64, "a wavefront adds the chunks");
 
 // ---- forward -----------------------------------------------------------------
 
@@ -339,7 +353,8 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
     constexpr int TEAMS = THREADS / L, N = kVec<X>, J = V / N, EMAX = L * V;
     // while tokens are routed: the candidates of each team; then the wavefronts' sums; then what ends the load
     constexpr size_t LISTS = sizeof(uint64_t) * TEAMS * EMAX, COLS = sizeof(float) * (THREADS / 64) * EMAX;
-    constexpr size_t ENDS = sizeof(EndScratch<THREADS>), MORE = LOAD ? (COLS > ENDS ? COLS : ENDS) : 0;
+    constexpr int CHUNK = EMAX < 64 ? EMAX : 64;
+    constexpr size_t ENDS = LOAD == 2 ? sizeof(EndScratch<THREADS, CHUNK>) : 0, MORE = LOAD ? (COLS > ENDS ? COLS : ENDS) : 0;
     __shared__ __align__(16) char pool[LISTS > MORE ? LISTS : MORE];
     __shared__ int32_t hist[LOAD ? EMAX : 1];
     __shared__ float slots[TEAMS][EMAX < GA_MAX_TOPK ? EMAX : GA_MAX_TOPK];
@@ -521,10 +536,10 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
     }
     if constexpr (LOAD == 2) {
         if (!last_of(q.done + 1, gridDim.x)) return;
-        auto& end_scratch = *reinterpret_cast<EndScratch<THREADS>*>(pool);
+        auto& end_scratch = *reinterpret_cast<EndScratch<THREADS, CHUNK>*>(pool);
         end_rest(la, q, end_scratch);
         double loss = 0.0;
-        for (int c = 0; c * kChunk < E; ++c) loss += end_chunk(la, q, end_scratch, c);
+        for (int c = 0; c * CHUNK < E; ++c) loss += end_chunk(la, q, end_scratch, c);
         if (threadIdx.x == 0) la.load.loss[0] = (float)loss;
     }
 }
@@ -700,8 +715,15 @@ int64_t parts_of(int64_t tokens, int teams, int64_t most) {
     return p < 1 ? 1 : p;
 }
 
-// Up to this many elements of partial loads the workgroup that ends last adds them itself.
-constexpr int64_t kOneLaunch = 8192;
+// Few partial loads are added by the workgroup that ends last, in one launch.  Against two launches, us (calls one after the
+// other in a graph): 64 tokens x 8 experts (1 row of partial loads) 7.3, 8.0; 2048 x 64 (64 rows) 10.9, 11.8; 512 x 128 (32) 10.7,
+// 12.3; but 4096 x 64 (128) 12.9, 12.0; 65536 x 8 (256) 14.7, 10.6; 256 x 256 (16) 17.2, 14.5.
+constexpr int64_t kOneRows = 64, kOneExperts = 128, kOneElements = 4096;
+
+// Up to this many rows a workgroup of the load's end takes 64 experts, else 16: few workgroups exchange their parts of the
+// loss sooner, many share long columns.  64 against 16, us: 1024 x 64 (8 rows) 11.2, 13.1; 512 x 128 (4) 12.2, 12.8; 8192 x 64
+// (64) 12.7, 13.7; 16384 x 64 (128) 15.6, 14.2; 131072 x 256 (256) 51.6, 45.6.
+constexpr int64_t kWideEnd = 64;
 
 template <int X>
 hipError_t router_fwd(const Router& r, const RouteArgs& args, hipStream_t s) {
@@ -718,10 +740,13 @@ hipError_t router_fwd(const Router& r, const RouteArgs& args, hipStream_t s) {
             return hipGetLastError();
         }
         q.parts = (int32_t)parts_of(a.per_worker, kThreads / L, r.rows / r.W);
-        if (r.W * q.parts * (int64_t)r.E <= kOneLaunch) {
-            hipLaunchKernelGGL((k_route<X, L, V, 2, kThreads>), dim3((unsigned)(r.W * q.parts)), dim3(kThreads), 0, s, a, la,
-                               q, r.normalize);
-            return hipGetLastError();
+        if constexpr (L * V <= kOneExperts) {
+            const int64_t few = (int64_t)r.W * q.parts;
+            if (few <= kOneRows && few * r.E <= kOneElements) {
+                hipLaunchKernelGGL((k_route<X, L, V, 2, kThreads>), dim3((unsigned)few), dim3(kThreads), 0, s, a, la, q,
+                                   r.normalize);
+                return hipGetLastError();
+            }
         }
         q.parts = (int32_t)parts_of(a.per_worker, kLoadThreads / L, r.rows / r.W);
         const int64_t rows = (int64_t)r.W * q.parts;
@@ -729,7 +754,10 @@ hipError_t router_fwd(const Router& r, const RouteArgs& args, hipStream_t s) {
                            r.normalize);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k_load_end, dim3((unsigned)((r.E + kChunk - 1) / kChunk) + 1), dim3(kEndThreads), 0, s, la, q);
+        if (rows <= kWideEnd)
+            hipLaunchKernelGGL(k_load_end<64>, dim3((unsigned)((r.E + 63) / 64) + 1), dim3(kEndThreads), 0, s, la, q);
+        else
+            hipLaunchKernelGGL(k_load_end<16>, dim3((unsigned)((r.E + 15) / 16) + 1), dim3(kEndThreads), 0, s, la, q);
         return hipGetLastError();
     });
 }
