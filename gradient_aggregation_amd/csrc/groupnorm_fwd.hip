@@ -6,6 +6,10 @@
 // threads give the mean m; with d = m - shift a thread's squares about m are
 // s2 - 2 d s1 + count d^2, and its deviations from m, s1 - count d, add up to what
 // m's roundings left, which corrects it.
+//
+// What bounds it, on bf16 with silu: small images (1 x 64 x 1280: 6.2 us of one kernel) the chain load, exchange, store; large
+// ones (4 x 65536 x 256) two readings and one writing, 26 us at 5.2 TB/s for the statistics and 43 us at 6.3 TB/s for y,
+// whose exponentials and reciprocals alone take 27.
 #include "groupnorm.h"
 
 namespace ga {
@@ -257,7 +261,8 @@ __global__ __launch_bounds__(T) void k_gn_fwd(GnArgs a, GnShape h) {
 }
 
 // ---- images that do not stay in registers ------------------------------------
-// Two kernels with the same workgroups on the same parts of the images: the statistics of each part, then y.
+// Two kernels with the same workgroups on the same parts of the images: the statistics of each part, then y.  Images of up
+// to about 128 MB are in the last-level cache when the second reads them.
 
 // Of a part (and piece) of a group: the mean m + off and the sum of squares about it.
 typedef f32x4 GnRecord;

@@ -698,7 +698,7 @@ ga_status ga_layernorm_backward(const ga_layernorm* ln, int64_t rows, const ga_r
 /* Most channels of a group norm. */
 #define GA_MAX_CHANNELS 65536
 
-/* none: z.  relu: z where z > 0, else 0.  silu: z / (1 + exp(-z)). */
+/* none: z.  relu: 0 where z < 0, else z (a NaN stays one).  silu: z / (1 + exp(-z)). */
 typedef enum { GA_ACT_NONE = 0, GA_ACT_RELU = 1, GA_ACT_SILU = 2 } ga_activation;
 
 /* Images, channels last: channel c of position s of sample n is at data +
@@ -718,8 +718,9 @@ typedef struct ga_groupnorm ga_groupnorm;
  * Group norm over images of `channels` channels of x_dtype in `groups` groups of
  * consecutive channels, with weight and bias vectors of p_dtype (GA_FP32 or
  * x_dtype), followed by an activation, on the current device.  The handle owns
- * a workspace that both passes use; backward == 0 leaves out the part that only
- * the backward pass needs (then ga_groupnorm_backward refuses the handle).
+ * a workspace that both passes use, of 16 MiB; with backward != 0 another 16 MiB
+ * or less (4096 bytes for each channel) of partial weight gradients, without
+ * which ga_groupnorm_backward refuses the handle.
  * GA_ERR_INVALID: channels < 1, groups < 1 or no divisor of channels, a type or an
  * activation that is not listed; GA_ERR_UNSUPPORTED: channels > GA_MAX_CHANNELS.
  */
@@ -783,7 +784,7 @@ typedef struct ga_router ga_router;
  * Router of E = `experts` experts, k of them to a token, for the tokens of
  * `workers` workers, on the current device.  x_dtype: the logits' type (any
  * ga_dtype).  normalize: the gates of a token sum to 1.  The handle owns the
- * workspace of the counts.
+ * workspace of the counts, at most 8.5 MB.
  * GA_ERR_INVALID: experts < 1, k outside [1, experts], workers < 1, an unknown type
  * or balance; GA_ERR_UNSUPPORTED: experts > GA_MAX_EXPERTS, k > GA_MAX_TOPK,
  * workers > GA_MAX_WORKERS.
@@ -833,14 +834,16 @@ typedef struct {
  *     the logits, so that it does not underflow); 0 at no expert.
  * A token is absent where d_mask ([tokens] bytes, or NULL) is 0, or where all its
  * logits are -infinity: its gates and lse are 0, its experts, if selected, are -1, and it
- * counts nowhere, whatever its logits are.
+ * counts nowhere, whatever its logits are.  Softmax, gates and lse are binary32
+ * (exponential, logarithm and reciprocal within 1 ulp of the hardware's).
  * With load (NULL: not formed), and F, P, n its counts, probs and tokens (of all
  * workers together, or of each worker, whose losses are then averaged):
  *   balance = E / (k n^2) * sum_e F_e P_e (1 where both are uniform)
  *   z = sum(lse^2) / n          (no tokens: both 0)
  * A NaN or +infinity makes its token's gates and lse, and the losses, NaN; the
- * squares of an lse past 1.8e19 are infinite.  Sums
- * are in binary32 over a workgroup's tokens, in binary64 beyond, in a fixed order.
+ * losses are written as binary32, and infinite past it.  Sums of probabilities are
+ * in binary32 over a workgroup's tokens, in binary64 beyond, those of squares in
+ * binary64, all in a fixed order.
  *   logits: rows of E.  routing->gates and ->lse may be NULL; with load, all of
  *   its pointers are needed.
  * With load, it uses the handle's workspace: not concurrently with another such
@@ -858,8 +861,9 @@ ga_status ga_router_forward(const ga_router* router, int64_t tokens, const ga_ro
  *   balance * (balance loss) + z * (z loss) + sum of dgates * gates
  * to the logits, the experts and counts held constant, rounded once to x_dtype.
  * routing and d_slope are those of the forward pass over the same logits and
- * mask; p is formed from its lse, and so off by 2^-24 of lse's size.  d_dgates: [tokens][k] binary32, or NULL for 0.  d_slope: NULL only where
- * balance and z are 0.  dlogits may be logits itself.  Absent tokens: 0.
+ * mask; p is formed from its lse, and so off by 2^-24 of lse's size.  d_dgates:
+ * [tokens][k] binary32, or NULL for 0.  d_slope: NULL only where balance and z are
+ * 0.  dlogits may be logits itself.  Absent tokens: 0.
  * routing->gates is read with `normalize` and d_dgates only.  A worker's mean gradient
  * is `workers` times the gradient of the mean over all: scale balance and z so
  * where the workers' gradients are averaged.
