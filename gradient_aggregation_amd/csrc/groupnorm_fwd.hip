@@ -5,7 +5,9 @@
 // its squares too) and their squares as its vectors arrive.  The sums of all
 // threads give the mean m; with d = m - shift a thread's squares about m are
 // s2 - 2 d s1 + count d^2, and its deviations from m, s1 - count d, add up to what
-// m's roundings left, which corrects it.
+// m's roundings left, which corrects it.  A thread of many rows moves its sums to
+// their own mean after 8, 16, 32, ... of them: a shift that is an outlier, A from
+// the rest, would add A^2 with every row, and so take the others' bits.
 //
 // What bounds it, on bf16 with silu: small images (1 x 64 x 1280: 6.2 us of one kernel) the chain load, exchange, store; large
 // ones (4 x 65536 x 256) two readings and one writing, 26 us at 5.2 TB/s for the statistics and 43 us at 6.3 TB/s for y,
@@ -20,11 +22,12 @@ template <int MODE, int N>
 struct Moments {
     static constexpr int M = MODE == kWhole ? 1 : N;    // a sum of the vector, or one for each channel
     float shift[M], s1[M], s2[M];
+    float past[M];         // squares of the rows before the last move, about shift
     int rows;
 
     __device__ __forceinline__ Moments() : rows(0) {
 #pragma unroll
-        for (int e = 0; e < M; ++e) shift[e] = s1[e] = s2[e] = 0.f;
+        for (int e = 0; e < M; ++e) shift[e] = s1[e] = s2[e] = past[e] = 0.f;
     }
 
     template <bool RAGGED>
@@ -68,6 +71,45 @@ struct Moments {
             s1[k] += d;
             s2[k] = fmaf(d, d, s2[k]);
         }
+    }
+
+    // Moves sum k of `count` values by about `by`, in roundings of the deviations' size only.
+    __device__ __forceinline__ void move(int k, float by, float count) {
+        const float to = shift[k] + by, d = to - shift[k], left = fmaf(-count, d, s1[k]);
+        past[k] += fmaf(-d, s1[k] + left, s2[k]);             // s2 - 2 d s1 + count d^2
+        shift[k] = to;
+        s1[k] = left;
+        s2[k] = 0.f;
+    }
+
+    // The sums to the mean of what they hold (a reciprocal's ulp off, which the sums then have).
+    template <bool RAGGED>
+    __device__ __forceinline__ void recentre(const Place<MODE, N>& p) {
+        const int left = RAGGED && p.left < N ? p.left : N;
+        if constexpr (MODE == kWhole) {
+            const float count = (float)(rows * left);
+            move(0, s1[0] * __builtin_amdgcn_rcpf(count), count);
+        } else {
+            const float count = (float)rows, inv = __builtin_amdgcn_rcpf(count);
+            const int border = MODE == kSpan ? p.border < left ? p.border : left : 0;
+            float first = 0.f, second = 0.f;
+            if constexpr (MODE == kSpan) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    first += e < border ? s1[e] : 0.f;
+                    second += e >= border && e < left ? s1[e] : 0.f;
+                }
+                first *= inv * __builtin_amdgcn_rcpf((float)border);
+                second *= left > border ? inv * __builtin_amdgcn_rcpf((float)(left - border)) : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) move(e, MODE == kMany ? s1[e] * inv : e < border ? first : second, count);
+        }
+    }
+
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int e = 0; e < M; ++e) s2[e] += past[e];
     }
 };
 
@@ -307,6 +349,8 @@ __global__ __launch_bounds__(T) void k_gn_stats(GnArgs a, GnShape h, GnRecord* _
                 for (int i = 0; i + 1 < rows.full; ++i) {
                     load(y, kAhead);
                     add(x, kAhead, i == 0);
+                    // after 8, 16, 32, ... rows: of an outlier's square in the first of them, 8 at most, each later one adds less
+                    if (kAhead * (i + 1) >= 8 && (i & (i + 1)) == 0) t.template recentre<RAGGED>(p);
 #pragma unroll
                     for (int k = 0; k < kAhead; ++k) x[k] = y[k];
                 }
@@ -318,6 +362,7 @@ __global__ __launch_bounds__(T) void k_gn_stats(GnArgs a, GnShape h, GnRecord* _
                 add(x, rows.tail, true);
             }
         });
+        t.end();
     }
     // of the groups' values in this part and slab
     const float count = (float)positions_of(h, o.part) * (float)(h.pieces == 1 ? h.cg : p.channels), inv = 1.f / count;

@@ -734,9 +734,10 @@ void ga_groupnorm_destroy(ga_groupnorm* gn);
  * Forward over `samples` samples of `positions` positions (either 0: nothing is
  * launched).  For each sample and group, over its positions and channels:
  *   mean = sum(x)/n, rstd = 1/sqrt(sum((x - mean)^2)/n + eps)      (binary32, the
- *          sums about a value of the data itself: a group far from zero, constant
- *          or nearly so, loses nothing; deviations past 1.8e19 have squares past
- *          binary32, and rstd is 0 or NaN)
+ *          sums about values of the data itself, moved as they grow: neither a
+ *          group's distance from zero nor an outlier in it costs more than some tens
+ *          of roundings; deviations past 1.8e19 have squares past binary32, and rstd
+ *          is 0 or NaN)
  *   y = activation((x - mean) * rstd * gamma + beta), rounded once to x_dtype
  * gamma, beta: [channels] of p_dtype, or NULL for 1 and 0.  d_mean, d_rstd:
  * [samples][groups] binary32, or NULL.  y may be x itself.
