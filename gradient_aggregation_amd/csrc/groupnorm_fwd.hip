@@ -116,9 +116,9 @@ struct Moments {
 // What a thread's groups have over all of a workgroup's values: m, the mean as first rounded; off, the mean of the
 // deviations from it; sq, the sum of their squares (not yet less count * off^2).  Constant groups add up exactly.
 template <int MODE, int N, int T>
-__device__ __forceinline__ void statistics(const Moments<MODE, N>& t, float base, float inv, float (&m)[Moments<MODE, N>::M],
-                                           float (&off)[Moments<MODE, N>::M], float (&sq)[Moments<MODE, N>::M], float* lds,
-                                           const GnShape& h, const Place<MODE, N>& p) {
+__device__ __forceinline__ void statistics(const Moments<MODE, N>& t, const float (&base)[Moments<MODE, N>::M], float inv,
+                                           float (&m)[Moments<MODE, N>::M], float (&off)[Moments<MODE, N>::M],
+                                           float (&sq)[Moments<MODE, N>::M], float* lds, const GnShape& h, const Place<MODE, N>& p) {
     constexpr int M = Moments<MODE, N>::M, SEGMENTS = MODE == kSpan ? 2 : 1;
     const int all = h.Q * h.sg;
     if constexpr (MODE != kMany) {
@@ -189,11 +189,11 @@ __device__ __forceinline__ void statistics(const Moments<MODE, N>& t, float base
         const float count = (float)t.rows;
         float x[1][M];
 #pragma unroll
-        for (int e = 0; e < M; ++e) x[0][e] = t.rows ? fmaf(count, t.shift[e] - base, t.s1[e]) : 0.f;
+        for (int e = 0; e < M; ++e) x[0][e] = t.rows ? fmaf(count, t.shift[e] - base[e], t.s1[e]) : 0.f;
         sum_groups<N, T>(x, tile, res, h, p);
 #pragma unroll
         for (int e = 0; e < M; ++e) {
-            m[e] = fmaf(res[p.here ? p.q * h.sg + p.group(h, e) : 0], inv, base);
+            m[e] = fmaf(res[p.here ? p.q * h.sg + p.group(h, e) : 0], inv, base[e]);
             x[0][e] = t.rows ? fmaf(-count, m[e] - t.shift[e], t.s1[e]) : 0.f;
         }
         sum_groups<N, T>(x, tile, res + all, h, p);
@@ -215,13 +215,39 @@ size_t lds_of_statistics(GnMode mode, const GnShape& h, int N, int T) {
     return sizeof(float) * (tile + 3 * (size_t)h.Q * h.sg);
 }
 
-// The slab's first value, which its threads share; it may not be finite, and another group's.
-template <int X, int MODE, int N>
-__device__ __forceinline__ float base_value(uint64_t image, const Place<MODE, N>& p) {
-    if constexpr (MODE != kMany) return 0.f;
-    const float b = load_one<X>(image + (uint64_t)p.c0 * kSize<X>);
-    return fabsf(b) < INFINITY ? b : 0.f;
-}
+// Where a vector holds several groups: of each element's group the first value, which the group's threads share.  A value
+// of another group would not do: its distance may be any number of deviations.  (Not finite: nor is then the group's mean.)
+// They are in the vector itself, but for the first element's.
+template <int X, int MODE, bool TINY, int N>
+struct Base {
+    Raw<X, N> x;
+    float before;
+
+    __device__ __forceinline__ Base(uint64_t image, const GnShape& h, const Place<MODE, N>& p) {
+        if constexpr (MODE == kMany) {
+            const int c = p.c0 + p.group(h, 0) * h.cg;
+            load_vector<X, TINY>(x, image, h, p);
+            before = load_one<X>(image + (uint64_t)((c < h.C ? c : h.C - 1) * kSize<X>));
+        }
+    }
+
+    template <int M>
+    __device__ __forceinline__ void get(float (&base)[M], const GnShape& h, const Place<MODE, N>& p) {
+        if constexpr (MODE == kMany) {
+            float f[N];
+            into_row<X, true>(x, p.past);
+            x.widen(f);
+            int g = p.group(h, 0);
+            base[0] = before;
+#pragma unroll
+            for (int e = 1; e < N; ++e) {
+                const int last = g;
+                g = p.group(h, e);
+                base[e] = g != last ? f[e] : base[e - 1];
+            }
+        }
+    }
+};
 
 // y of one vector: (x - m) * scale + bias, activated.
 template <int X, bool RAGGED, bool STREAM, int MODE, int N>
@@ -253,7 +279,7 @@ __global__ __launch_bounds__(T) void k_gn_fwd(GnArgs a, GnShape h) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
         if (i < most) load_vector<X, false>(x[i], i + 1 < most ? xr + (uint64_t)(i * step) : xl, h, p);
-    const float base = base_value<X>(image, p);
+    Base<X, MODE, false, N> first(image, h, p);
     float scale[N], bias[N];
     load_weight<X>(scale, a.gamma, h, p.c, 1.f);
     load_weight<X>(bias, a.beta, h, p.c, 0.f);
@@ -272,7 +298,8 @@ __global__ __launch_bounds__(T) void k_gn_fwd(GnArgs a, GnShape h) {
             }
         });
     }
-    float m[M], off[M], sq[M];
+    float base[M], m[M], off[M], sq[M];
+    first.get(base, h, p);
     statistics<MODE, N, T>(t, base, h.inv_n, m, off, sq, lds, h, p);
     if (!in) return;
 #pragma unroll
@@ -317,7 +344,7 @@ __global__ __launch_bounds__(T) void k_gn_stats(GnArgs a, GnShape h, GnRecord* _
     const Place<MODE, N> p(h, o.slab);
     const uint64_t image = reinterpret_cast<uint64_t>(a.x.data) + (uint64_t)(o.n * a.x.sample);
     const bool in = p.here && p.left > 0;
-    const float base = base_value<X>(image, p);
+    Base<X, MODE, TINY, N> first(image, h, p);
     Moments<MODE, N> t;
     const Rows rows(h, o.part, p.r);
     if (in && rows.full + rows.tail > 0) {
@@ -366,7 +393,8 @@ __global__ __launch_bounds__(T) void k_gn_stats(GnArgs a, GnShape h, GnRecord* _
     }
     // of the groups' values in this part and slab
     const float count = (float)positions_of(h, o.part) * (float)(h.pieces == 1 ? h.cg : p.channels), inv = 1.f / count;
-    float m[M], off[M], sq[M];
+    float base[M], m[M], off[M], sq[M];
+    first.get(base, h, p);
     statistics<MODE, N, T>(t, base, inv, m, off, sq, lds, h, p);
     if (!in || p.r != 0) return;
     const int K = h.parts * h.pieces, k = o.part * h.pieces + (h.pieces == 1 ? 0 : o.slab % h.pieces);

@@ -1,7 +1,7 @@
 """How near group norm's statistics and outputs come to their definitions, with bounds
 that hold for what the kernels claim and for little more: an outlier among a thread's
-first values, in every way that groups lie on vectors, held in registers and in two
-kernels.
+first values, groups beside ones of another size, in every way that groups lie on vectors,
+held in registers and in two kernels.
 
 U = 2^-24.  A mean is off by at most some roundings of the deviations that it is a mean
 of: the sums of thousands of roundings of either sign, divided by the count, stay below
@@ -68,6 +68,16 @@ MANY_ROWS = [(512, 16384, 16, 2, "fp32"), (512, 21760, 12, 2, "fp32"), (512, 163
 def test_plain(ga, shape, x):
     N, S, C, G = shape
     check(ga, normal(N, S, C).to(DT[x]), G)
+
+
+@pytest.mark.parametrize("shape", REGISTERS + KERNELS)
+def test_beside_groups_of_another_size(ga, shape):
+    """Each group's sums are about values of its own, whatever its neighbours in a vector hold."""
+    N, S, C, G = shape
+    x = normal(N, S, C).reshape(N, S, G, C // G)
+    x[:, :, ::2] = 1e9 * (1 + 0.1 * x[:, :, ::2])
+    x[:, :, 1::2] += 1000
+    check(ga, x.reshape(N, S, C), G)
 
 
 @pytest.mark.parametrize("x", ["fp32", "fp16", "bf16"])
