@@ -59,7 +59,7 @@ struct Router {
     float* d_probs;        // [rows][E]
     int32_t* d_counts;     // [rows][E]
     int32_t* d_tokens;     // [rows]
-    uint32_t* d_done;      // [2] workgroups that have ended; 0 between calls
+    uint32_t* d_done;      // [2] counts of workgroups that have ended; 0 between calls
 };
 
 constexpr int kRouterRows = 256;

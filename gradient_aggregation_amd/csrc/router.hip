@@ -16,6 +16,7 @@
 // (131072 x 256 bf16: 31 us, 4.7 TB/s).  Small calls: the launch and a chain of some 5 us.
 #include <type_traits>
 
+#include "arrival.h"
 #include "layers.h"
 #include "rowvec.h"
 
@@ -169,7 +170,7 @@ struct LoadParts {
     double* squares;       // [rows]
     int32_t* tokens;       // [rows]
     double* dots;          // a part of the balance loss for each chunk of experts
-    uint32_t* done;        // [2]; 0 between calls
+    uint32_t* done;        // [2], of the parts of the loss and of the partial loads (see arrival); 0 between calls
     int32_t parts;
 };
 
@@ -310,19 +311,20 @@ __device__ __forceinline__ void end_rest(const LossArgs& a, const LoadParts& q, 
     if (all) a.load.slope[a.E] = (float)(2.0 * share_of(all_n));
 }
 
-// Whether this workgroup is the last of n to get here; what the others stored before is then visible.  Each wavefront
-// waits for its own stores: the barrier does not, and the release, thread 0's, writes back what the cache holds then.
-__device__ __forceinline__ bool last_of(uint32_t* done, uint32_t n) {
+// Whether this workgroup is the last of the launch to get here; what the others stored before is then visible.  Each
+// wavefront waits for its own stores: the barrier does not, and the release, thread 0's, writes back what the cache holds
+// then.
+__device__ __forceinline__ bool last_of(uint32_t* done) {
     __shared__ uint32_t last;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
-        last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT) + 1 == n;
+        const uint32_t mine = arrival(blockIdx.x, gridDim.x);
+        last = __hip_atomic_fetch_add(done, mine, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT) + mine == 0u;
     }
     __syncthreads();
     if (!last) return false;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    if (threadIdx.x == 0) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return true;
 }
 
@@ -349,13 +351,13 @@ __global__ __launch_bounds__(kEndThreads) void k_load_end(LossArgs a, LoadParts 
     if (threadIdx.x == 0) {
         __hip_atomic_store(q.dots + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        last = __hip_atomic_fetch_add(q.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 2 == gridDim.x ? 1u : 0u;
+        const uint32_t mine = arrival(blockIdx.x, gridDim.x - 1);
+        last = __hip_atomic_fetch_add(q.done, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + mine == 0u ? 1u : 0u;
     }
     if (__builtin_amdgcn_readfirstlane(last) == 0u) return;
     asm volatile("" ::: "memory");
     double loss = threadIdx.x + 1 < gridDim.x
                       ? __hip_atomic_load(q.dots + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
-    if (threadIdx.x == 0) __hip_atomic_store(q.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     loss = wave_sum_f64(loss);
     if (threadIdx.x == 0) a.load.loss[0] = (float)loss;
 }
@@ -552,7 +554,7 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
         }
     }
     if constexpr (LOAD == 2) {
-        if (!last_of(q.done + 1, gridDim.x)) return;
+        if (!last_of(q.done + 1)) return;
         auto& end_scratch = *reinterpret_cast<EndScratch<THREADS, CHUNK>*>(pool);
         end_rest(la, q, end_scratch);
         double loss = 0.0;

@@ -848,8 +848,8 @@ typedef struct {
  *   logits: rows of E.  routing->gates and ->lse may be NULL; with load, all of
  *   its pointers are needed.
  * With load, it uses the handle's workspace: not concurrently with another such
- * call on the same handle (issue them on one stream or order them with events; an
- * overlap can spoil the calls after it too).
+ * call on the same handle (issue them on one stream or order them with events;
+ * calls that overlap give wrong results).
  * Errors: GA_ERR_INVALID: a NULL argument, tokens < 0 or not a multiple of
  * workers, rows that overlap; GA_ERR_ALIGN: a buffer not aligned to its
  * element; GA_ERR_UNSUPPORTED: tokens * k past 2^31 - 1.
