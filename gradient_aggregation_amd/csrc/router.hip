@@ -4,7 +4,8 @@
 // A token's row of E logits is read once, by a team of lanes that keeps it in registers: its largest logit, the sum of
 // exp(l - largest), and from them lse = largest + log(sum) and p = exp(l - largest) / sum.  The k largest are found by
 // rank: logits as whole numbers of the same order, a bound that at least k of them reach, those above it written to the
-// team's list in LDS with their index, and for each of the list the number of larger ones, which is its place.  Counts go to
+// team's list in LDS with their index, and for each of the list the number of larger ones, which is its place (or, where
+// equal logits make the list long, the largest left of it, k times).  Counts go to
 // a histogram in LDS (whole numbers, in any order), probabilities are summed in each lane's registers over the tokens that
 // it takes.  A workgroup leaves one partial row of both; a second kernel adds the rows in order, and ends the losses.
 //
@@ -162,6 +163,23 @@ __device__ __forceinline__ uint32_t kth_of_groups(const uint32_t (&key)[V], uint
     }
     return bound;
 }
+
+// Whether, instead of ranking so many candidates against each other, found^2 / L comparisons to a lane, the k largest are
+// found one after the other, each in found / L steps and two exchanges: where many logits are equal (all, where a router's
+// weights are still 0).  Ranked against not, us, with a load: 65536 x 256, 8 of them (16 lanes), 25 candidates 42, 43; 33:
+// 56, 47; 256: 497, 99.  16384 x 1024, 32 of them (64 lanes), 100: 63, 97; 145: 111, 113; 1024: 1543, 245.  131072 x 64 bf16,
+// 1 of them (8 lanes), 12: 24, 23; 64: 136, 29.
+template <int L>
+__device__ __forceinline__ bool too_many(int found, int k) {
+    return found > L + 2 * k;
+}
+
+// A candidate is its key and, below, the complement of its index, so that among equal ones the lowest index is the largest;
+// the upper bits of that give way to a place where it is known.
+__device__ __forceinline__ uint32_t placed(uint32_t index, int place) { return (index & 1023u) | (uint32_t)place << 10; }
+__device__ __forceinline__ int place_of(uint32_t index) { return (int)(index >> 10); }
+__device__ __forceinline__ int index_of(uint32_t index) { return (int)(~index & 1023u); }
+static_assert(GA_MAX_EXPERTS <= 1024, "an index of 10 bits");
 
 // Where the partial loads of the workgroups lie: row = worker * parts + part.
 struct LoadParts {
@@ -472,16 +490,38 @@ __global__ __launch_bounds__(THREADS) void k_route(RouteArgs a, LossArgs la, Loa
             about = best > kLeast ? value_of(best) : 0.f;
         }
         float chosen = 0.f;
+        const bool many = a.select && too_many<L>(found, k);
+        if (many) {
+            // one after the other: a lane's largest candidate, the team's, whose lane notes its place
+            for (int j = 0; j < k; ++j) {
+                uint64_t best = 0;
+                int from = ln;
+                for (int c = ln; c < found; c += L) {
+                    const uint64_t x = list[c];
+                    if ((int32_t)x < 0 && x > best) {
+                        best = x;
+                        from = c;
+                    }
+                }
+                const uint32_t key = team_max<L>((uint32_t)(best >> 32));
+                const uint32_t index = team_max<L>((uint32_t)(best >> 32) == key ? (uint32_t)best : 0u);
+                if (best == ((uint64_t)key << 32 | index)) list[from] = (uint64_t)key << 32 | placed(index, j);
+            }
+        }
         for (int c = ln; c < found; c += L) {
             int rank = c, at = -1;
             float g = 0.f;
             if (a.select) {
                 const uint64_t mine = list[c];
-                rank = 0;
+                if (many) {
+                    rank = place_of((uint32_t)mine);
+                } else {
+                    rank = 0;
 #pragma unroll 4
-                for (int j = 0; j < found; ++j) rank += list[j] > mine ? 1 : 0;
+                    for (int j = 0; j < found; ++j) rank += list[j] > mine ? 1 : 0;
+                }
                 if (rank >= k) continue;
-                at = (int)~(uint32_t)mine;
+                at = index_of((uint32_t)mine);
                 g = __builtin_amdgcn_exp2f((value_of((uint32_t)(mine >> 32)) - top) * kLog2e);
                 experts[rank] = at;
             } else {

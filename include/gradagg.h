@@ -829,6 +829,8 @@ typedef struct {
  *   select != 0: experts <- the k largest logits in descending order, among equal
  *     ones the lowest index first.  A logit of -infinity is never selected, nor
  *     is a NaN: where fewer than k are left, the remaining experts are -1.
+ *     (Tokens with many logits equal to their k-th largest take up to some five
+ *     times as long as others.)
  *   select == 0: experts is read (a selection made elsewhere; one outside [0, E)
  *     is no expert, the same one twice counts twice).
  *   gates <- p at the experts; with `normalize`, divided by their sum (formed from
