@@ -147,3 +147,40 @@ def test_samples_of_a_worker_in_a_workgroup(ga, shape, per, x):
     N, S, C, G = shape
     a, dy, gamma, beta = inputs(N, S, C, x, "fp32", "plain")
     check_backward(ga, dy, a, gamma, beta, G, "silu", N // per)
+
+
+@pytest.mark.parametrize("shape,W", [((16, 64, 128, 8), 16), ((16, 36, 64, 32), 4), ((6, 1443, 250, 25), 3), ((3, 5000, 64, 32), 1),
+                                     ((4, 3025, 96, 8), 2), ((520, 16384, 16, 2), 1), ((64, 4096, 24, 8), 8)])
+def test_sums_of_the_backward_pass(ga, shape, W):
+    """Sums of terms of either sign, in chains of at most r = 256 rows (2 to 4 vectors' terms a row for a group, and then
+    trees): each addition's rounding is up to U of a partial sum that grows with the root of its terms, so that the sum's error
+    has a deviation of U sqrt(r / 6) sqrt(sum of squares); the terms' own, 4 U each, add 4 U / sqrt(3) of it.  Six deviations:
+    60 U; and 8 U of the sum itself, as for the means above."""
+    N, S, C, G = shape
+    a, dy, gamma, _ = inputs(N, S, C, "fp32", "fp32", "plain")
+    gn = ga.GroupNorm(C, G)
+    mean, rstd = torch.empty(2, N, G, device="cuda")
+    y, dx = torch.empty_like(a), torch.empty_like(a)
+    dg, db = torch.empty(2, W, C, device="cuda")
+    gn.forward(a, gamma, None, y, mean, rstd)
+    gn.backward(dy, a, gamma, None, mean, rstd, dx, dg, db, workers=W)
+    sums = torch.zeros(4, W, C, dtype=torch.float64, device="cuda")
+    for n in range(N):
+        xh = (a[n:n + 1].double() - spread(mean[n:n + 1].double(), C)) * spread(rstd[n:n + 1].double(), C)
+        d = dy[n:n + 1].double()
+        w = n * W // N
+        for k, t in enumerate((d * xh, d)):
+            sums[k, w] += t.sum((0, 1))
+            sums[2 + k, w] += t.square().sum((0, 1))
+        if n > 8 and n < N - 2:
+            continue
+        h = d * gamma.double()
+        R, count = spread(rstd[n:n + 1].double(), C), S * C // G
+        m1, m2 = grouped(h, G), grouped(h * xh, G)
+        e1, e2 = (60 * U * (grouped(t.square(), G) / count).sqrt() + 8 * U * m.abs() for t, m in ((h, m1), (h * xh, m2)))
+        m1, m2, e1, e2 = (spread(t, C) for t in (m1, m2, e1, e2))
+        want = R * (h - m1 - xh * m2)
+        err = R * (e1 + xh.abs() * e2 + 8 * U * (h.abs() + m1.abs() + (xh * m2).abs()))
+        assert bool(((dx[n:n + 1].double() - want).abs() <= err).all())
+    for got, want, squares in ((dg, sums[0], sums[2]), (db, sums[1], sums[3])):
+        assert bool(((got.double() - want).abs() <= 60 * U * squares.sqrt() + 8 * U * want.abs()).all())
