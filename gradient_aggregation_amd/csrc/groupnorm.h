@@ -279,7 +279,7 @@ inline int pow2_floor(int64_t x) {
     return p;
 }
 
-constexpr int kMostGroups = 512;     // of a slab; of a workgroup's samples twice that
+constexpr int kMostSums = 1024;       // groups of a workgroup's samples together; a slab has 64 at most (see choose, lay_wide)
 constexpr int64_t kMostBlocks = 1 << 20;
 
 inline GnShape shape_of(const GroupNorm& n, int64_t S) {
@@ -340,7 +340,7 @@ inline bool lay(GnShape& h, int sg, int N, int T, int V, int64_t samples) {
     h.slabs = (int)ceil_div(h.G, sg);
     // several samples at once where one leaves threads idle, as long as the workgroups fill the chip
     int64_t Q = T / (h.nv * h.R);
-    if (Q > 2 * kMostGroups / sg) Q = 2 * kMostGroups / sg;
+    if (Q > kMostSums / sg) Q = kMostSums / sg;
     const int64_t most = samples * h.slabs / 1024;
     if (Q > most) Q = most;
     h.Q = Q < 1 ? 1 : (int)Q;
@@ -365,7 +365,6 @@ inline int choose(GnShape& h, int N, const TeamSize (&teams)[K], int half, int64
     int64_t sg = unit;
     while (sg * h.cg < 4 * N && sg < h.G) sg += unit;
     if (sg > h.G) sg = h.G;
-    if (sg > kMostGroups) return -1;
     const bool halves = sg * h.cg % (4 * N) == 0;
     if (!halves && samples * h.S * h.C > (int64_t)(8 << 20) / 16 * N) return -1;
     for (int k = 0; k < K; ++k)
@@ -385,11 +384,11 @@ inline void lay_wide(GnShape& h, int N, int T, int64_t samples) {
         h.slabs = h.G * h.pieces;
     } else {
         int64_t sg = line / gcd_of(h.cg, line);
-        if (sg > h.G || sg * h.cg > 8 * line || sg > kMostGroups) {
+        if (sg > h.G || sg * h.cg > 8 * line) {
             const int unit = N / gcd_of(h.cg, N);
             sg = h.C <= 4 * line ? h.G : unit;
             while (sg * h.cg < line && sg < h.G) sg += unit;
-            while (ceil_div(sg * h.cg, N) > T || sg > kMostGroups) sg -= sg > unit ? unit : 1;
+            while (ceil_div(sg * h.cg, N) > T) sg -= sg > unit ? unit : 1;
         }
         if (sg > h.G) sg = h.G;
         h.sg = (int)sg;

@@ -326,7 +326,7 @@ template <int X, int MODE, bool TINY, int T>
 __global__ __launch_bounds__(T) void k_gn_dx(GnArgs a, GnShape h, GnSpan span, const GnSums* __restrict__ records,
                                              const float* __restrict__ rows_in, uint32_t images) {
     constexpr int N = kVec<X>, M = MODE == kWhole ? 1 : N;
-    extern __shared__ __align__(16) float lds[];        // the means of h and h * xh of the slab's groups
+    extern __shared__ __align__(16) float lds[];        // the means of h and h * xh of the slab's groups, 64 at most
     if (blockIdx.x >= images) {
         end_params<T>(a, h, span.w0, rows_in, blockIdx.x - images, lds);
         return;
@@ -503,8 +503,7 @@ hipError_t gn_bwd(const GroupNorm& n, const GnArgs& a, hipStream_t s) {
                 constexpr bool TINY = decltype(t)::value;
                 hipLaunchKernelGGL((k_gn_sums<X, MODE, TINY, T>), dim3(blocks), dim3(T), bytes, s, a, h, span, records,
                                    n.d_rows, direct);
-                const size_t some = sizeof(float) * (h.sg > T ? 2 * h.sg : 2 * T);
-                hipLaunchKernelGGL((k_gn_dx<X, MODE, TINY, T>), dim3(images + ends), dim3(T), some, s, a, h, span, records,
+                hipLaunchKernelGGL((k_gn_dx<X, MODE, TINY, T>), dim3(images + ends), dim3(T), sizeof(float) * 2 * T, s, a, h, span, records,
                                    n.d_rows, images);
             };
             if (h.C < N) launch(std::integral_constant<int, kMany>{}, std::integral_constant<bool, true>{});
