@@ -4,9 +4,10 @@
 // what dx needs (a group's means of h = dz * gamma and h * xh are those sums weighted
 // by gamma) and the weight gradients (those sums added over the samples).
 //
-// What bounds it: 16 x 16384 x 128 bf16 with silu, 34 us for the sums (4.0 TB/s; the two transcendental instructions and some
-// twelve others to an element) and 34 us for dx (6.0 TB/s); 6 x 1443 x 250 binary32 13 and 8.5 us, filling and draining;
-// 4 x 36 x 1024, held in registers, 6.8 us of one kernel.
+// What bounds it: 16 x 16384 x 128 bf16 with silu, 34 to 36 us for the sums (3.7 TB/s; 20 vector instructions to an element,
+// two of them transcendental: 63% of the time of the SIMDs, whose two wavefronts wait for the rest) and 34 us for dx (5.9
+// TB/s); 6 x 1443 x 250 binary32 13 and 8.5 us, few rows to a thread and a slab that leaves half of its threads idle;
+// 4 x 36 x 1024, held in registers, 6.7 us of one kernel.
 #include "groupnorm.h"
 #include "training.h"
 

@@ -12,9 +12,10 @@
 // Backward, with h_e = balance * slope_e (+ dgate at its expert) and p = exp(l - lse) formed again:
 //   dl_e = p_e (h_e - sum(h p) + z slope_z lse), and with normalised gates + gate_j (dgate_j - sum(dgate gate)) at expert j.
 //
-// What bounds it: forward the instructions of softmax and selection, not memory (131072 x 256 binary32, 8 of them: 45 us at
-// 3.2 TB/s, its bytes alone 23; 65536 x 64 bf16, 6 of them: 14 us for 12 MB); backward HBM and the exponentials
-// (131072 x 256 bf16: 31 us, 4.7 TB/s).  Small calls: the launch and a chain of some 5 us.
+// What bounds it: forward vector instructions, 66 to 75% of the SIMDs' time, and waits of the 16 wavefronts that the lists
+// leave room for on a CU (131072 x 256 binary32, 8 of them: 34 instructions to a logit, 45 us at 3.2 TB/s, its bytes alone 23;
+// 65536 x 64 bf16, 6 of them: 64 to a logit, 14 us for 12 MB); backward HBM and the exponentials (131072 x 256 bf16: 31 us,
+// 4.7 TB/s).  Small calls: the launch and a chain of some 5 us.
 #include <type_traits>
 
 #include "arrival.h"
@@ -780,8 +781,9 @@ int64_t parts_of(int64_t tokens, int teams, int64_t most) {
 constexpr int64_t kOneRows = 64, kOneExperts = 128, kOneElements = 4096;
 
 // Up to this many rows a workgroup of the load's end takes 64 experts, else 16: few workgroups exchange their parts of the
-// loss sooner, many share long columns.  64 against 16, us: 1024 x 64 (8 rows) 11.2, 13.1; 512 x 128 (4) 12.2, 12.8; 8192 x 64
-// (64) 12.7, 13.7; 16384 x 64 (128) 15.6, 14.2; 131072 x 256 (256) 51.6, 45.6.
+// loss sooner, many share long columns.  64 against 16, us, bf16: 256 x 256 (4 rows) 14.9, 15.6; 64 x 1024 (4) 14.1, 14.8;
+// 1024 x 256 (16) 15.2, 15.9; 8192 x 64 (64) 13.0, 14.0; 4096 x 256 (64) 16.7, 16.3; 16384 x 64 (128) 15.8, 14.5; 8192 x 128
+// (128) 17.0, 13.9; 65536 x 64 (256) 23.3, 18.7.
 constexpr int64_t kWideEnd = 64;
 
 template <int X>

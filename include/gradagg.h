@@ -698,7 +698,8 @@ ga_status ga_layernorm_backward(const ga_layernorm* ln, int64_t rows, const ga_r
 /* Most channels of a group norm. */
 #define GA_MAX_CHANNELS 65536
 
-/* none: z.  relu: 0 where z < 0, else z (a NaN stays one).  silu: z / (1 + exp(-z)). */
+/* none: z.  relu: 0 where z < 0, else z (a NaN stays one).  silu: z / (1 + exp(-z)), or 0 where
+   that is below 1e-36 in size. */
 typedef enum { GA_ACT_NONE = 0, GA_ACT_RELU = 1, GA_ACT_SILU = 2 } ga_activation;
 
 /* Images, channels last: channel c of position s of sample n is at data +
