@@ -758,6 +758,8 @@ ga_status ga_groupnorm_forward(const ga_groupnorm* gn, int64_t samples, int64_t 
  * beta, dz = dy * activation'(z) (relu: 0 where z <= 0) and h = dz * gamma:
  *   dx = rstd * (h - mean_group(h) - xh * mean_group(h * xh))
  *   dgamma[w] = sum of dz * xh,  dbeta[w] = sum of dz   over the samples of worker w
+ * xh is formed from the binary32 mean that is given, and off by its rounding, 2^-24
+ * |mean| * rstd.
  * The samples form `workers` runs of samples/workers consecutive ones, each with
  * its own weight gradients: d_dgamma, d_dbeta: [workers][channels] of dp_dtype
  * (any ga_dtype), or both NULL.  All sums are binary32, each in a fixed order.  With
